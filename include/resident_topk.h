@@ -34,7 +34,8 @@
  *     (rt_engine_create_shared).
  *   - Results are best-first.  Indices are int32 (0-based row / element
  *     positions), so n is limited to 2^31 - 1.
- *   - Inputs must be NaN-free; the comparator does not order NaN.
+ *   - Inputs must be NaN-free; the comparator does not order NaN (int8 rows and
+ *     row sampling say themselves what they do with NaN).
  */
 #ifndef RESIDENT_TOPK_H
 #define RESIDENT_TOPK_H
@@ -55,7 +56,12 @@ typedef enum {
     RT_EHIP = 4    /* a HIP runtime call failed; see rt_last_hip_error */
 } rt_status;
 
-typedef enum { RT_DTYPE_INT32 = 0, RT_DTYPE_FLOAT32 = 1 } rt_dtype;
+typedef enum {
+    RT_DTYPE_INT32 = 0,
+    RT_DTYPE_FLOAT32 = 1,
+    RT_DTYPE_BFLOAT16 = 2, /* int8 rows and row sampling only */
+    RT_DTYPE_FLOAT16 = 3   /* int8 rows and row sampling only */
+} rt_dtype;
 
 /* Similarity used by search_resident_metric ("GPU-Resident Top-K for Agentic
  * RAG", section 4, Step 2: the scoring kernel computes an inner product and,
@@ -271,6 +277,107 @@ rt_status topk_select_noalloc(const void *values, int32_t dtype, int64_t n, int3
                               void *out_values, void *stream);
 
 /*
+ * int8 rows: products of activations with a matrix kept as int8 rows, with one
+ * fp32 scale per row on both sides (a language model's output head or any
+ * projection; the int8 counterpart of the batched scores).  No engine: device
+ * pointers are on the calling thread's current HIP device, as is `stream`, and
+ * nothing is allocated.  Leading dimensions (ld*) count elements between rows
+ * and are at least the row length; anything between a row's end and the next
+ * row is neither read for its value nor written.  m = 0 returns RT_OK and does nothing.
+ * Outputs must not overlap inputs, each other or the workspace.
+ * Speed: rows whose addresses are all 16-byte aligned (pointer and ld multiples
+ * of 16 bytes) take the direct-to-LDS kernels; others are read unaligned.
+ *
+ * rt_quantize_rows_int8: q[i][j] = x[i][j] / scale[i] rounded to the nearest
+ * whole number, ties to even, decided on the exact quotient;
+ * scale[i] = max_j |x[i][j]| / 127 in fp32 (so |q| <= 127).  A row whose scale
+ * would fall below the smallest normal fp32 (2^-126), zero rows among them, is
+ * stored as zeros with scale 0.  A row holding an infinity or NaN is stored as
+ * zeros with scale NaN, so that every product with it is NaN.
+ *   x      device, m rows of k elements (fp32, bf16 or fp16), aligned to its type
+ *   q      device, m rows of k int8;  scale  device, m fp32
+ * RT_EINVAL: null pointer, dtype, m < 0, m > 2^31-1, k < 1, k > 65536, ld < k,
+ * ld > 2^31-1, a pointer not aligned to its type.
+ */
+rt_status rt_quantize_rows_int8(const void *x, int32_t dtype, int64_t m, int32_t k, int64_t ldx, int8_t *q,
+                                int64_t ldq, float *scale, void *stream);
+
+/*
+ * out[i][j] = (sum_l a[i][l] b[j][l]) * a_scale[i] * b_scale[j] (+ bias[j]),
+ * i < m, j < n: the sum is exact in 32-bit integers (int8 values -128..127,
+ * k <= 65536), the rest fp32, rounded once to the output type.
+ *   a, b             device, m and n rows of k int8
+ *   a_scale, b_scale device, m and n fp32;  bias  device, n fp32, or NULL
+ *   out              device, m rows of n elements of out_dtype (fp32, bf16, fp16)
+ * RT_EINVAL as above, and for n < 1, n > 2^31-1 or m n > 2^37.  Asynchronous on
+ * `stream`; may be captured into a graph; calls may overlap freely.
+ */
+rt_status rt_matmul_int8(const int8_t *a, int64_t lda, const float *a_scale, const int8_t *b, int64_t ldb,
+                         const float *b_scale, const float *bias, void *out, int32_t out_dtype, int64_t ldo,
+                         int64_t m, int64_t n, int32_t k, void *stream);
+
+/*
+ * rt_quantize_rows_int8 of the activations x (m rows of k, fp32, bf16 or fp16)
+ * followed by rt_matmul_int8 with the int8 rows w (n rows of k): the same
+ * numbers as the two calls.  `workspace` is device memory of at least
+ * rt_linear_int8_workspace(m, k) bytes, 16-byte aligned, that the call uses for
+ * the quantised activations until its work on `stream` is done: calls that may
+ * run at the same time (other streams, other graphs) need one each.
+ * rt_linear_int8_workspace returns 0 for m = 0, -1 for sizes the call refuses.
+ */
+int64_t rt_linear_int8_workspace(int64_t m, int32_t k);
+rt_status rt_linear_int8(const void *x, int32_t dtype, int64_t ldx, const int8_t *w, int64_t ldw,
+                         const float *w_scale, const float *bias, void *out, int32_t out_dtype, int64_t ldo,
+                         int64_t m, int64_t n, int32_t k, void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * Row sampling: one token per row of logits, drawn with given random numbers.
+ * The settings of a row: from the arrays where they are not NULL (device, r
+ * entries each), else from the plain values.
+ */
+typedef struct {
+    float temperature; /* above 0; anything else (0, negative, NaN) takes the row's first token of the order */
+    int32_t top_k;     /* 0 or less: off */
+    float top_p;       /* 1 or more: off; 0 or less, or NaN: the first token only */
+    float min_p;       /* 0 or less: off; above 1, or NaN: the first token only */
+    const float *temperatures;
+    const int32_t *top_ks;
+    const float *top_ps;
+    const float *min_ps;
+} rt_sample_settings;
+
+/*
+ * For each row of r x v logits: tokens are ordered as topk_select orders values
+ * (larger first, -0.0 ties +0.0, ties to the lower index); NaN counts as -inf.
+ * Token i weighs w_i = exp((x_i - max x) / temperature) (where the largest
+ * logit is +inf: 1 for every +inf, 0 for the rest).  Kept are
+ *   top_k  the first top_k tokens of the order,
+ *   top_p  of those, the shortest prefix whose weights sum to at least top_p
+ *          times theirs,
+ *   min_p  tokens with w_i >= min_p,
+ * all three together; the first token of the order is always kept.  With S the
+ * sum of the kept weights, the row's token is the first, in index order, at
+ * which the running sum of kept weights exceeds u S (u >= 1: the last with any
+ * weight; u < 0 or NaN: the first), and its probability w / S.  A row with no
+ * logit above -inf gets token -1 and probability 0.
+ * Sums are taken in 64-bit whole multiples of 2^-min(46, 62 - ceil(log2 v)) of
+ * the largest weight: the same inputs always give the same token.
+ *   logits    device, r rows of v elements (fp32, bf16 or fp16), ld elements apart
+ *   u         device, r fp32 in [0, 1)
+ *   out_token device, r int32;  out_prob  device, r fp32, or NULL
+ *   workspace device, at least rt_sample_rows_workspace(r, v) bytes, 16-byte
+ *             aligned (NULL if that is 0), used until the call's work is done:
+ *             calls that may run at the same time need one each
+ * r = 0 returns RT_OK and does nothing.  RT_EINVAL: null pointer, dtype, r < 0,
+ * r > 2^31-1, v < 1, v > 2^31-1, ld < v, ld > 2^31-1, a misaligned pointer, a
+ * workspace too small.  Asynchronous on `stream`; may be captured into a graph.
+ */
+int64_t rt_sample_rows_workspace(int64_t r, int64_t v);
+rt_status rt_sample_rows(const void *logits, int32_t dtype, int64_t r, int64_t v, int64_t ld, const float *u,
+                         const rt_sample_settings *settings, int32_t *out_token, float *out_prob, void *workspace,
+                         int64_t workspace_bytes, void *stream);
+
+/*
  * Dynamic batching of concurrent single-query searches ("GPU-Resident Top-K
  * for Agentic RAG", section 1: many small agents retrieving against one
  * corpus; section 9: no concurrency between queries inside one engine).
@@ -362,7 +469,7 @@ rt_status rt_engine_info(const rt_engine *e, int64_t *out7);
  * Host-side argument checks, exported so they can be tested without a GPU.
  * They apply exactly the rules the entry points above apply before enqueuing
  * anything, given the engine limits and resident sizes as plain numbers
- * (resident_n = 0 means no corpus).  Pointers are only tested for NULL.
+ * (resident_n = 0 means no corpus).  Pointers are only tested for NULL and alignment.
  */
 rt_status rt_check_create(int64_t max_n, int32_t max_d, int32_t max_k, int32_t max_q);
 rt_status rt_check_upload(int64_t max_n, int32_t max_d, const void *corpus, int64_t n, int32_t d);
@@ -372,6 +479,14 @@ rt_status rt_check_search_metric(int32_t max_k, int32_t max_q, int64_t resident_
                                  int32_t q, int32_t k, int32_t metric, const void *out_idx, const void *out_scores);
 rt_status rt_check_select(int32_t max_k, const void *values, int32_t dtype, int64_t n, int32_t k,
                           const void *out_idx, const void *out_values);
+rt_status rt_check_quantize_rows_int8(const void *x, int32_t dtype, int64_t m, int32_t k, int64_t ldx,
+                                      const void *q, int64_t ldq, const void *scale);
+rt_status rt_check_matmul_int8(const void *a, int64_t lda, const void *a_scale, const void *b, int64_t ldb,
+                               const void *b_scale, const void *bias, const void *out, int32_t out_dtype,
+                               int64_t ldo, int64_t m, int64_t n, int32_t k);
+rt_status rt_check_sample_rows(const void *logits, int32_t dtype, int64_t r, int64_t v, int64_t ld, const void *u,
+                               const rt_sample_settings *settings, const void *out_token, const void *out_prob,
+                               const void *workspace, int64_t workspace_bytes);
 
 /*
  * The two constants of search_resident_filtered's bound for depth d, host-only

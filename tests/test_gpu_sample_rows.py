@@ -1,0 +1,258 @@
+"""Row sampling on the GPU against the plain 64-bit definition: every filter
+and their combinations, one logit to long rows, ties, masks, infinities and
+NaN, extreme settings, strides, streams and graphs.
+
+The kernel's sums are off by at most what row_oracle.draw works out from the
+unit of its weights; a row whose decisions all stay further than that from a
+border must give the same token.  The rows here do (asserted)."""
+import numpy as np
+import pytest
+
+import row_oracle
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+from top_search_resident_amd import ResidentTopKError, linear_int8, quantize_rows_int8, sample_rows  # noqa: E402
+
+TYPES = {"fp32": torch.float32, "bf16": torch.bfloat16, "fp16": torch.float16}
+NAN, INF = float("nan"), float("inf")
+
+
+def per_row(value, r):
+    return value.cpu().numpy() if isinstance(value, torch.Tensor) else [value] * r
+
+
+def check(x, u, exact_ties=False, **settings):
+    """x, u on the CPU; runs the kernel and compares every row."""
+    gpu = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in settings.items()}
+    token, prob = sample_rows(x if x.is_cuda else x.cuda(), u.cuda(), **gpu)
+    token, prob = token.cpu().numpy(), prob.cpu().numpy()
+    r, v = x.shape
+    rows = x.double().cpu().numpy()
+    s = {k: per_row(settings.get(k, d), r) for k, d in
+         (("temperature", 1.0), ("top_k", 0), ("top_p", 1.0), ("min_p", 0.0))}
+    for i in range(r):
+        e, p, margin, error = row_oracle.draw(rows[i], u[i].item(), s["temperature"][i], int(s["top_k"][i]),
+                                       s["top_p"][i], s["min_p"][i])
+        if not exact_ties:
+            assert margin > error, ("the test's own row sits on a border", i, margin, error)
+        assert token[i] == e, (i, token[i], e, margin)
+        # the sum's error and one rounding to fp32
+        assert abs(prob[i] - p) <= p * (2.0 ** -24 + error) * 1.01 + 2.0 ** -149, (i, prob[i], p)
+    return token, prob
+
+
+def logits(r, v, dtype, seed, spread=2.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(r, v, generator=g) * spread).to(TYPES[dtype]), torch.rand(r, generator=g)
+
+
+FILTERS = [dict(), dict(temperature=0.7), dict(top_k=5), dict(top_k=1000), dict(top_p=0.9), dict(top_p=0.3),
+           dict(min_p=0.05), dict(top_k=40, top_p=0.8), dict(top_p=0.95, min_p=0.01), dict(top_k=3000, top_p=0.97),
+           dict(temperature=1.5, top_k=300, top_p=0.9, min_p=0.002), dict(temperature=0.05, top_k=50, top_p=0.99)]
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("v", [1, 2, 63, 1000, 8193, 50001])
+@pytest.mark.parametrize("f", range(len(FILTERS)))
+def test_filters(dtype, v, f):
+    x, u = logits(5, v, dtype, 100 * v + f)
+    check(x, u, **FILTERS[f])
+
+
+@pytest.mark.parametrize("dtype,v", [("bf16", 131072), ("fp32", 262145), ("fp16", 1000003)])
+@pytest.mark.parametrize("f", [0, 4, 7, 8, 9, 10])
+def test_long_rows(dtype, v, f):
+    x, u = logits(2, v, dtype, v + f)
+    check(x, u, **FILTERS[f])
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_settings_of_each_row(dtype):
+    r = 40
+    x, u = logits(r, 3001, dtype, 77)
+    g = torch.Generator().manual_seed(8)
+
+    def pick(values, dt):
+        return torch.tensor(values, dtype=dt)[torch.randint(0, len(values), (r,), generator=g)]
+
+    check(x, u, temperature=pick([0.0, 0.5, 1.0, 2.0, -1.0], torch.float32),
+          top_k=pick([0, 1, 2, 50, 2000, 5000, -3], torch.int32),
+          top_p=pick([1.0, 0.5, 0.9, 0.0, 2.0], torch.float32), min_p=pick([0.0, 0.1, 0.001, 1.0], torch.float32))
+
+
+@pytest.mark.parametrize("top_k", [1, 2, 3, 7, 2500, 4095, 4096])
+def test_ties_keep_the_lower_index(top_k):
+    """All logits equal, and two levels: whole weights make every border exact."""
+    v = 4096
+    x = torch.zeros(8, v)
+    x[4:] = torch.where(torch.arange(v) % 3 == 0, 1.5, -40.0)
+    u = torch.tensor([0.0, 0.25, 0.5, 0.999] * 2)
+    token, prob = check(x, u, exact_ties=True, top_k=top_k)
+    assert (token[:4] == [int(q * top_k) for q in u[:4].tolist()]).all()
+    assert np.all(prob[:4] == np.float32(1.0 / top_k))
+
+
+@pytest.mark.parametrize("top_p,kept", [(0.5, 2048), (0.25, 1024), (1.0, 4096), (0.125, 512)])
+def test_flat_rows_split_exactly(top_p, kept):
+    x = torch.full((3, 4096), -7.25)
+    token, prob = check(x, torch.tensor([0.0, 0.5, 0.99]), exact_ties=True, top_p=top_p)
+    assert np.all(prob == np.float32(1.0 / kept)) and token[1] == kept // 2
+
+
+def test_ties_of_signed_zeros_and_many_equal_logits():
+    x = torch.zeros(2, 20000)
+    x[:, ::2] = -0.0
+    x[1, 7] = 0.5
+    check(x, torch.tensor([0.3, 0.7]), exact_ties=True, top_k=33)
+    # bf16 logits with a few values each held by thousands: the border lies inside a tie
+    g = torch.Generator().manual_seed(4)
+    y = torch.randint(-4, 5, (6, 60000), generator=g).to(torch.bfloat16)
+    for s in (dict(top_k=10), dict(top_k=9000), dict(top_p=0.7), dict(top_p=0.999), dict(top_k=20000, top_p=0.5),
+              dict(min_p=0.1)):
+        check(y, torch.rand(6, generator=g), **s)
+
+
+def test_masked_infinite_and_nan_logits():
+    v = 5000
+    g = torch.Generator().manual_seed(6)
+    x = torch.randn(12, v, generator=g) * 3
+    x[0] = -INF                               # nothing left
+    x[1] = NAN
+    x[2, 1:] = -INF                           # one token left
+    x[3, :-1] = NAN
+    x[4, ::2] = -INF
+    x[5, 1::2] = NAN
+    x[6, 100] = INF                           # one infinite logit takes all
+    x[7, [9, 4000, 77]] = INF                 # three share
+    x[8] = torch.finfo(torch.float32).min     # masks of the lowest value
+    x[9] = torch.finfo(torch.float32).min
+    x[9, 123] = 4.0
+    x[10] = torch.finfo(torch.float32).max
+    x[11, :4990] = -INF
+    u = torch.rand(12, generator=g)
+    for s in (dict(), dict(top_k=20), dict(top_p=0.9), dict(min_p=0.1), dict(temperature=0.0), dict(top_k=4999),
+              dict(temperature=0.3, top_k=30, top_p=0.5, min_p=0.01)):
+        token, prob = check(x, u, exact_ties=True, **s)
+        assert (token[:2] == -1).all() and (prob[:2] == 0).all()
+        assert token[2] == 0 and token[3] == v - 1 and token[6] == 100 and token[9] == 123
+        assert token[7] in (9, 77, 4000)
+
+
+@pytest.mark.parametrize("s", [dict(temperature=1e-30), dict(temperature=1e-45), dict(temperature=1e30),
+                               dict(temperature=INF, top_k=7), dict(temperature=NAN), dict(temperature=-1.0),
+                               dict(top_p=1e-9), dict(top_p=0.0), dict(top_p=-1.0), dict(top_p=NAN), dict(top_p=7.0),
+                               dict(min_p=1.0), dict(min_p=1.5), dict(min_p=NAN), dict(min_p=1e-40), dict(min_p=-1.0),
+                               dict(top_k=2 ** 40), dict(top_k=-5)])
+def test_extreme_settings(s):
+    x, u = logits(4, 900, "fp32", 12)
+    check(x, u, exact_ties=True, **s)
+
+
+def test_random_numbers_at_the_ends():
+    x, _ = logits(6, 700, "fp32", 13)
+    x[:, :5] = -INF
+    x[:, -5:] = -INF
+    u = torch.tensor([0.0, -1.0, NAN, 1.0, 2.0, 1.0 - 2.0 ** -24])
+    token, _ = check(x, u, exact_ties=True)
+    assert (token[:3] == 5).all() and (token[3:5] == 694).all()
+
+
+def test_every_kept_token_can_be_drawn():
+    """A sweep of u over one row gives each kept token its share of the sweep."""
+    x = torch.tensor([[0.0, 3.0, 1.0, 2.5, -1.0, 2.0]]).repeat(1000, 1)
+    u = (torch.arange(1000) + 0.5) / 1000
+    token, prob = sample_rows(x.cuda(), u.cuda(), top_k=4)
+    token, prob = token.cpu().numpy(), prob.cpu().numpy()
+    assert set(token) == {1, 2, 3, 5}
+    w = {1: 1.0, 3: np.exp(-0.5), 5: np.exp(-1.0), 2: np.exp(-2.0)}
+    for i, q in w.items():
+        share = q / sum(w.values())
+        assert abs(np.mean(token == i) - share) <= 2e-3  # a border moves one of 1000 steps at each end
+        assert np.all(np.abs(prob[token == i] - share) <= share * 2.0 ** -23)
+    assert (np.diff(token) >= 0).all()  # index order
+
+
+def test_strides_and_given_outputs():
+    x, u = logits(9, 1111, "bf16", 15)
+    store = torch.full((9, 1300), 50.0).to(torch.bfloat16)
+    store[:, 3:3 + 1111] = x
+    view = store.cuda()[::2, 3:3 + 1111]
+    tok = torch.full((5,), -7, dtype=torch.int32, device="cuda")
+    prob = torch.empty(5, device="cuda")
+    got = sample_rows(view, u[::2].contiguous().cuda(), top_k=30, out_token=tok, out_prob=prob)
+    assert got[0] is tok and got[1] is prob
+    check(view, u[::2].contiguous(), top_k=30)
+    e, _ = sample_rows(x.cuda()[::2].contiguous(), u[::2].contiguous().cuda(), top_k=30)
+    assert torch.equal(tok, e)
+
+
+def test_empty_batch():
+    t, p = sample_rows(torch.empty(0, 10, device="cuda"), torch.empty(0, device="cuda"))
+    assert t.shape == (0,) and p.shape == (0,)
+
+
+def test_streams_at_once_and_same_answer_each_time():
+    x, u = logits(3, 200000, "fp32", 16)
+    y, w = logits(70, 30000, "bf16", 17)
+    jobs = [(x.cuda(), u.cuda(), dict(top_p=0.95)), (y.cuda(), w.cuda(), dict(top_k=50, top_p=0.9))]
+    first = [sample_rows(a, b, **s) for a, b, s in jobs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [(i, sample_rows(*jobs[i][:2], **jobs[i][2], stream=streams[i])) for _ in range(5) for i in range(2)]
+    torch.cuda.synchronize()
+    for i, g in got:
+        assert torch.equal(g[0], first[i][0]) and torch.equal(g[1], first[i][1])
+
+
+@pytest.mark.parametrize("r,v", [(1, 32000), (1, 300000), (33, 5000)])
+def test_captured_and_replayed(r, v):
+    x, u = logits(r, v, "fp32", 18)
+    x, u = x.cuda(), u.cuda()
+    s = dict(temperature=0.9, top_k=100, top_p=0.9)
+    sample_rows(x, u, **s)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        tok, prob = sample_rows(x, u, **s)
+    for seed in range(4):
+        nx, nu = logits(r, v, "fp32", 50 + seed)
+        x.copy_(nx)
+        u.copy_(nu)
+        graph.replay()
+        got = tok.clone(), prob.clone()
+        eager = sample_rows(x, u, **s)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], eager[0]) and torch.equal(got[1], eager[1])
+        check(nx, nu, **s)
+
+
+def test_head_product_then_draw():
+    """Hidden states through an int8 output head, then one token each: the
+    tokens are those the plain definitions give for the head's own logits."""
+    g = torch.Generator().manual_seed(20)
+    w, sw = quantize_rows_int8((torch.randn(5003, 768, generator=g) * 0.05).cuda())
+    hidden = torch.randn(6, 768, generator=g).to(torch.bfloat16).cuda()
+    scores = linear_int8(hidden, w, sw, out_dtype=torch.float32)
+    q, s = row_oracle.quantize_rows(hidden.double().cpu().numpy())
+    y, prod = row_oracle.product(q, s, w.cpu().numpy(), sw.cpu().numpy())
+    assert (np.abs(scores.double().cpu().numpy() - y) <= 3.01 * 2.0 ** -24 * prod).all()
+    check(scores, torch.rand(6, generator=g), temperature=0.8, top_k=50, top_p=0.9)
+
+
+def test_rejects_bad_arguments():
+    x = torch.zeros(4, 32, device="cuda")
+    u = torch.zeros(4, device="cuda")
+    for bad in (lambda: sample_rows(x.double(), u), lambda: sample_rows(x.t(), u), lambda: sample_rows(x.cpu(), u),
+                lambda: sample_rows(x, u.cpu()), lambda: sample_rows(x, u.double()),
+                lambda: sample_rows(x, u, top_k=torch.ones(4, device="cuda")),
+                lambda: sample_rows(x[:1].expand(4, 32), u)):
+        with pytest.raises(TypeError):
+            bad()
+    for bad in (lambda: sample_rows(x, u[:3]), lambda: sample_rows(x[0], u),
+                lambda: sample_rows(x, u, temperature=torch.ones(5, device="cuda"))):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(ResidentTopKError):
+        sample_rows(torch.empty(4, 0, device="cuda"), u)

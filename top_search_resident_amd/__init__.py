@@ -10,6 +10,10 @@ library is not built.
     eng.upload_corpus_rowmajor(corpus)              # once; host or device fp32 [n, d]
     idx, scores = eng.search_resident(queries, k)   # device fp32 [q, d] -> [q, k] each
     idx, vals = eng.topk_select(values, k)          # device int32/fp32 [n] -> [k] each
+
+Without an engine: int8 rows and their products (quantize_rows_int8, matmul_int8,
+linear_int8), one token drawn per row of logits (sample_rows), and
+topk_select_noalloc.
 """
 import ctypes
 import threading
@@ -17,8 +21,11 @@ import weakref
 
 from . import _lib
 from ._lib import ResidentTopKError, RT_DTYPE_FLOAT32, RT_DTYPE_INT32, RT_METRIC_COSINE, RT_METRIC_DOT
+from .rows import (linear_int8, linear_int8_workspace, matmul_int8, quantize_rows_int8, sample_rows,
+                   sample_rows_workspace)
 
-__all__ = ["ResidentTopK", "ResidentTopKError", "Batcher", "topk_select_noalloc"]
+__all__ = ["ResidentTopK", "ResidentTopKError", "Batcher", "topk_select_noalloc", "quantize_rows_int8", "matmul_int8",
+           "linear_int8", "linear_int8_workspace", "sample_rows", "sample_rows_workspace"]
 
 
 _torch_module = None

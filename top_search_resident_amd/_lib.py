@@ -9,7 +9,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIBRARY = os.path.join(HERE, "libresident_topk.so")
 
 RT_OK, RT_EINVAL, RT_ESTATE, RT_ENOMEM, RT_EHIP = 0, 1, 2, 3, 4
-RT_DTYPE_INT32, RT_DTYPE_FLOAT32 = 0, 1
+RT_DTYPE_INT32, RT_DTYPE_FLOAT32, RT_DTYPE_BFLOAT16, RT_DTYPE_FLOAT16 = 0, 1, 2, 3
 RT_METRIC_DOT, RT_METRIC_COSINE = 0, 1
 
 # Every symbol include/resident_topk.h declares.
@@ -21,10 +21,19 @@ EXPORTS = (
     "rt_filter_bounds_batched", "rt_filter_bounds_fp8", "rt_set_filter_storage", "rt_filter_path_used",
     "rt_read_probe", "search_resident_filtered_metric", "topk_select_noalloc", "rt_cosine_score",
     "rt_filter_cosine_bounds", "rt_batcher_create", "rt_batcher_submit", "rt_batcher_wait", "rt_batcher_stats",
-    "rt_batcher_destroy",
+    "rt_batcher_destroy", "rt_quantize_rows_int8", "rt_matmul_int8", "rt_linear_int8", "rt_linear_int8_workspace",
+    "rt_sample_rows", "rt_sample_rows_workspace", "rt_check_quantize_rows_int8", "rt_check_matmul_int8",
+    "rt_check_sample_rows",
 )
 
 _lib = None
+
+
+class SampleSettings(ctypes.Structure):
+    """rt_sample_settings: plain values, and per-row device arrays where not NULL."""
+    _fields_ = [("temperature", ctypes.c_float), ("top_k", ctypes.c_int32), ("top_p", ctypes.c_float),
+                ("min_p", ctypes.c_float), ("temperatures", ctypes.c_void_p), ("top_ks", ctypes.c_void_p),
+                ("top_ps", ctypes.c_void_p), ("min_ps", ctypes.c_void_p)]
 
 
 class ResidentTopKError(RuntimeError):
@@ -87,6 +96,17 @@ def load():
         "rt_batcher_wait": ([vp, ctypes.c_uint64], ctypes.c_int),
         "rt_batcher_stats": ([vp, ctypes.POINTER(i64)], ctypes.c_int),
         "rt_batcher_destroy": ([vp], None),
+        "rt_quantize_rows_int8": ([vp, i32, i64, i32, i64, vp, i64, vp, vp], ctypes.c_int),
+        "rt_matmul_int8": ([vp, i64, vp, vp, i64, vp, vp, vp, i32, i64, i64, i64, i32, vp], ctypes.c_int),
+        "rt_linear_int8": ([vp, i32, i64, vp, i64, vp, vp, vp, i32, i64, i64, i64, i32, vp, i64, vp], ctypes.c_int),
+        "rt_linear_int8_workspace": ([i64, i32], i64),
+        "rt_sample_rows": ([vp, i32, i64, i64, i64, vp, ctypes.POINTER(SampleSettings), vp, vp, vp, i64, vp],
+                           ctypes.c_int),
+        "rt_sample_rows_workspace": ([i64, i64], i64),
+        "rt_check_quantize_rows_int8": ([vp, i32, i64, i32, i64, vp, i64, vp], ctypes.c_int),
+        "rt_check_matmul_int8": ([vp, i64, vp, vp, i64, vp, vp, vp, i32, i64, i64, i64, i32], ctypes.c_int),
+        "rt_check_sample_rows": ([vp, i32, i64, i64, i64, vp, ctypes.POINTER(SampleSettings), vp, vp, vp, i64],
+                                 ctypes.c_int),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)

@@ -68,4 +68,69 @@ rt_status rt_check_select(int32_t max_k, const void *values, int32_t dtype, int6
     return RT_OK;
 }
 
+static bool float_type(int32_t dtype) {
+    return dtype == RT_DTYPE_FLOAT32 || dtype == RT_DTYPE_BFLOAT16 || dtype == RT_DTYPE_FLOAT16;
+}
+
+static bool misaligned(const void *p, int32_t dtype) {
+    return (reinterpret_cast<uintptr_t>(p) & (dtype == RT_DTYPE_FLOAT32 ? 3u : 1u)) != 0;
+}
+
+static bool bad_ld(int64_t ld, int64_t row) { return ld < row || ld > rt::kMaxLd; }
+
+rt_status rt_check_quantize_rows_int8(const void *x, int32_t dtype, int64_t m, int32_t k, int64_t ldx,
+                                      const void *q, int64_t ldq, const void *scale) {
+    if (!float_type(dtype)) return RT_EINVAL;
+    if (m < 0 || m > kMaxN || k < 1 || k > rt::kMaxRowK) return RT_EINVAL;
+    if (bad_ld(ldx, k) || bad_ld(ldq, k)) return RT_EINVAL;
+    if (m == 0) return RT_OK;  // an empty tensor's address may be null
+    if (x == nullptr || q == nullptr || scale == nullptr) return RT_EINVAL;
+    if (misaligned(x, dtype) || misaligned(scale, RT_DTYPE_FLOAT32)) return RT_EINVAL;
+    return RT_OK;
+}
+
+rt_status rt_check_matmul_int8(const void *a, int64_t lda, const void *a_scale, const void *b, int64_t ldb,
+                               const void *b_scale, const void *bias, const void *out, int32_t out_dtype,
+                               int64_t ldo, int64_t m, int64_t n, int32_t k) {
+    if (!float_type(out_dtype)) return RT_EINVAL;
+    if (m < 0 || m > kMaxN || n < 1 || n > kMaxN || k < 1 || k > rt::kMaxRowK) return RT_EINVAL;
+    if (m * n > rt::kMaxProduct) return RT_EINVAL;
+    if (bad_ld(lda, k) || bad_ld(ldb, k) || bad_ld(ldo, n)) return RT_EINVAL;
+    if (m == 0) return RT_OK;
+    if (a == nullptr || a_scale == nullptr || b == nullptr || b_scale == nullptr || out == nullptr) return RT_EINVAL;
+    if (misaligned(a_scale, RT_DTYPE_FLOAT32) || misaligned(b_scale, RT_DTYPE_FLOAT32) ||
+        misaligned(bias, RT_DTYPE_FLOAT32) || misaligned(out, out_dtype))
+        return RT_EINVAL;
+    return RT_OK;
+}
+
+int64_t rt_linear_int8_workspace(int64_t m, int32_t k) {
+    if (m < 0 || m > kMaxN || k < 1 || k > rt::kMaxRowK) return -1;
+    return m * rt::int8_padded(k) + (4 * m + 15) / 16 * 16;
+}
+
+rt_status rt_check_sample_rows(const void *logits, int32_t dtype, int64_t r, int64_t v, int64_t ld, const void *u,
+                               const rt_sample_settings *settings, const void *out_token, const void *out_prob,
+                               const void *workspace, int64_t workspace_bytes) {
+    if (!float_type(dtype)) return RT_EINVAL;
+    if (r < 0 || r > kMaxN || v < 1 || v > kMaxN || bad_ld(ld, v)) return RT_EINVAL;
+    if (settings == nullptr) return RT_EINVAL;
+    if (r == 0) return RT_OK;
+    if (logits == nullptr || u == nullptr || out_token == nullptr) return RT_EINVAL;
+    if (misaligned(logits, dtype) || misaligned(u, RT_DTYPE_FLOAT32) || misaligned(out_token, RT_DTYPE_FLOAT32) ||
+        misaligned(out_prob, RT_DTYPE_FLOAT32) || misaligned(settings->temperatures, RT_DTYPE_FLOAT32) ||
+        misaligned(settings->top_ks, RT_DTYPE_FLOAT32) || misaligned(settings->top_ps, RT_DTYPE_FLOAT32) ||
+        misaligned(settings->min_ps, RT_DTYPE_FLOAT32))
+        return RT_EINVAL;
+    const int64_t need = rt_sample_rows_workspace(r, v);
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return RT_EINVAL;
+    if ((reinterpret_cast<uintptr_t>(workspace) & 15u) != 0) return RT_EINVAL;
+    return RT_OK;
+}
+
+int64_t rt_sample_rows_workspace(int64_t r, int64_t v) {
+    if (r < 0 || r > kMaxN || v < 1 || v > kMaxN) return -1;
+    return 0;
+}
+
 }  // extern "C"
