@@ -37,7 +37,8 @@ def draw(x, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
     tie that whole weights decide); error is how far the shares of sums of whole
     weights can be off: each weight by half a unit of 2^-shift of the largest and
     2^-46 of itself, so a sum z of n weights by n unit / 2 + z 2^-46, and a
-    running sum as a share of it by twice that over z."""
+    running sum as a share of it by twice that over z; where top-p takes its
+    sums from a histogram, 2^-37 of itself instead."""
     unit = 2.0 ** -min(46, 62 - int(np.ceil(np.log2(len(x)))))
     error = 0.0
     x = np.where(np.isnan(x), -np.inf, x.astype(np.float64))
@@ -59,7 +60,7 @@ def draw(x, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
         before = np.concatenate([[0.0], run[:-1]])
         z = run[-1]
         inside = before < p * z
-        error = (n * unit + z * 2.0 ** -45) / z
+        error = (n * unit + z * 2.0 ** -36) / z
         inside[0] = True
         if p > 0:
             margin = min(margin, np.min(np.abs(before[1:] - p * z)) / z if n > 1 else 1.0)

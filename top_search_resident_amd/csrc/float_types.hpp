@@ -13,11 +13,16 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-// 16 bytes from any address (gfx950 reads unaligned addresses in one load).
+// A pointer to global memory, said to the compiler: where it cannot see that (a
+// pointer out of a struct, through a loop) it reads with flat loads, which wait
+// for LDS operations, too, and keep no loads in flight beside them.
+template <typename T>
+using global_ptr = const __attribute__((address_space(1))) T *;
+
+// 16 bytes from any global address (gfx950 reads unaligned addresses in one load).
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
 __device__ __forceinline__ u32x4 load16(const void *p) {
-    u32x4 v;
-    __builtin_memcpy(&v, p, 16);
-    return v;
+    return *reinterpret_cast<global_ptr<u32x4_any>>((uintptr_t)p);
 }
 
 // Element i (a constant after unrolling) of 16 bytes of T, as fp32.

@@ -3,22 +3,27 @@
 //
 // Mathematics.  Order the tokens by (logit down, index up).  Every filter keeps
 // a prefix of that order, so a row is settled by one border element: the k-th,
-// or the first at which the running weight reaches top_p of the whole, or the
-// min-p logit.  The draw is the same question in index order: the first kept
-// element at which the running weight reaches floor(u S) + 1.  All three are
-// answered by find_first(): histogram the elements over 2048 bins of a
-// monotone key, find the bin in which the running sum crosses the target,
-// narrow to it and repeat until one element is left.  No sort.
+// the first at which the running weight reaches top_p of the whole, or the last
+// one at or above the min-p logit.  The draw asks the same in index order: the first kept
+// element at which the running weight reaches floor(u S) + 1.  Nothing is
+// sorted but short lists of candidates.
 //
 // Weights are whole multiples of 2^-shift of the largest (shift <= 46), from a
-// 64-bit exponential, and all sums are 64-bit integers: histogram atomics in
-// any order give the same sums, so the same inputs give the same token, and a
-// border decided in plain 64-bit floating point falls on the same side except
-// within about 2^-45 of the whole.
+// 64-bit exponential, and all sums are 64-bit integers: atomics in any order
+// give the same sums, so the same inputs give the same token, and a border
+// decided in plain 64-bit floating point falls on the same side unless it is
+// within about 2^-43 of the whole.
 //
-// One workgroup of 1024 threads per row.  It keeps the first kKeep 16-byte chunks of every
-// thread in registers (the whole row up to 8192 kKeep bytes... see launch) and
-// reads the rest again in each pass.
+// One workgroup of 1024 threads per row, a few passes over it:
+//   1. the largest logit, and each thread's own largest;
+//   2a. top-k up to 1024: k threads' largest logits reach a value that few
+//       elements reach; those go to a list, and the list settles the row;
+//   2b. otherwise a histogram of the weights, 32 bins an octave, one for each
+//       eighth of the row;
+//   3. the elements of the one bin that the border cuts go to a list, which
+//       finds the border;
+//   4. the eighths' kept weights (bins before the border's, and the list) say
+//       which eighth the draw falls into; only that one is read again.
 #include <hip/hip_runtime.h>
 
 #include "../../include/resident_topk.h"
@@ -30,9 +35,10 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kWaves = kThreads / 64;
-constexpr int kBins = 2048;  // two per thread
-constexpr int kList = 2048;  // candidates kept in LDS
-constexpr int kSegs = 1024;  // index segments of the draw over a row
+constexpr int kList = 2048;   // candidates kept in LDS
+constexpr int kSmall = 128;   // lists up to here are settled by comparing all pairs
+constexpr int kSegs = 8;      // parts of a row with a histogram each
+constexpr int kSearch = 2048; // bins of find_first, two per thread
 
 struct SampleArgs {
     const void *logits;
@@ -42,135 +48,217 @@ struct SampleArgs {
     int32_t *out_token;
     float *out_prob;
     int shift;  // weights are multiples of 2^-shift of the largest
+    // The quartic of Weights::unit with 2^shift multiplied in, 2^shift + 2^52, and
+    // 2^-shift: as arguments they reach the fmas in scalar registers.
+    double c4, c3, c2, c1, one, per_unit;
 };
 
-// Order of the elements as one 64-bit number, larger first: the logit's bits
-// made monotone, then the index from the top down.
-__device__ __forceinline__ uint64_t order_key(float x, uint32_t idx) {
-    const uint32_t b = __float_as_uint(x + 0.0f);  // -0.0 becomes +0.0
-    const uint32_t o = (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-    return (uint64_t(o) << 32) | uint32_t(~idx);
-}
-__device__ __forceinline__ float key_value(uint64_t key) {
-    const uint32_t o = uint32_t(key >> 32);
-    return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
+// ------------------------------------------------------------------- weights
+
+// exp((x - top) / T) as a whole multiple of 2^-shift.  In octaves, t = (x - top)
+// log2(e) / T = 47 (sigma - 1), with sigma clamped to [0, 1], which an fma does
+// at no cost: NaN gives 0, as anything 47 octaves or more down (weight 0).  Adding
+// 1.5 * 2^47 leaves round(32 t) in the low bits, -bin; the rest f (|f| <= 2^-6)
+// gives 2^f by a quartic fitted with its constant fixed at 1 (relative error
+// 2^-43.5), and a table in LDS the factor 2^(shift - bin / 32), 0 in the last
+// bin; adding 2^52 rounds to a whole number.  The largest logit is finite here
+// (a row whose largest is +inf takes draw_infinite).
+constexpr int kPerOctave = 32, kOctaves = 47, kMass = kOctaves * kPerOctave + 1;
+constexpr double kRound = 211106232532992.0;   // 1.5 * 2^47
+constexpr double kWhole = 4503599627370496.0;  // 2^52
+constexpr double kC4 = 0.009618187552583722, kC3 = 0.055504515561345676, kC2 = 0.24022650695390316,
+                 kC1 = 0.693147180535112;
+// Elements without weight would all add to one bin: they go to one of these by lane.
+constexpr int kSpread = 64, kStride = kMass + kSpread;
+
+typedef const __attribute__((address_space(3))) double *lds_doubles;
+
+// a b + c with c in scalar registers.  Written out because the compiler turns an
+// fma with a constant addend into a move of the constant and an fmac: two
+// instructions where the passes below are bound by their number.
+__device__ __forceinline__ double fma_scalar(double a, double b, double c) {
+    double d;
+    asm("v_fma_f64 %0, %1, %2, %3" : "=v"(d) : "v"(a), "v"(b), "s"(c));
+    return d;
 }
 
-// exp((x - top) / T) as a whole multiple of 2^-shift: 2^t with t = (x - top)
-// log2(e) / T, a polynomial of degree 9 for the fraction (relative error
-// 2^-46, coefficients fitted for the smallest largest relative error on
-// [-1/2, 1/2]) and the exponent added on; adding 2^52 rounds to a whole number.
 struct Weights {
-    float top;
-    double rate;  // log2(e) / T
-    int shift;
+    double top, rate;  // rate = log2(e) / (47 T)
+    lds_doubles zero;  // the factor of bin 0; bin b's is at zero[-b]
+    double c4, c3, c2, c1, one, per_unit;
 
-    __device__ __forceinline__ double power(float x) const {
-        const double t = fmax((double(x) - double(top)) * rate, -200.0);  // NaN and -inf give -200
-        const double n = __builtin_rint(t), f = t - n;
-        double p = 1.0150336908049256e-07;
-        p = fma(p, f, 1.3259405616920547e-06);
-        p = fma(p, f, 1.5252984837515096e-05);
-        p = fma(p, f, 0.00015403434948043135);
-        p = fma(p, f, 0.0013333557617606637);
-        p = fma(p, f, 0.009618129192067264);
-        p = fma(p, f, 0.055504108668685596);
-        p = fma(p, f, 0.24022650695649653);
-        p = fma(p, f, 0.693147180559871);
-        p = fma(p, f, 1.0000000000000127);
-        return __builtin_ldexp(p, int(n) + shift);
+    __device__ __forceinline__ int split(float x, double *f) const {  // -bin
+        const double sigma = fmin(fmax(fma(double(x) - top, rate, 1.0), 0.0), 1.0);
+        const double m = fma_scalar(sigma, double(kOctaves), kRound - kOctaves);
+        *f = fma(sigma, double(kOctaves), (kRound - kOctaves) - m);
+        return int(uint32_t(__builtin_bit_cast(uint64_t, m)));
+    }
+    __device__ __forceinline__ double power(float x, int *bin) const {  // 2^f, and -bin
+        double f;
+        *bin = split(x, &f);
+        return fma(fma_scalar(fma_scalar(fma_scalar(f, kC4, kC3), f, kC2), f, kC1), f, 1.0);
     }
     __device__ __forceinline__ uint64_t operator()(float x) const {
-        const double y = power(x) + 4503599627370496.0;
-        const uint64_t w = __builtin_bit_cast(uint64_t, y) & 0x000fffffffffffffull;
-        return x >= top ? (uint64_t(1) << shift) : w;
+        int bin;
+        const double p = power(x, &bin);
+        return __builtin_bit_cast(uint64_t, fma_scalar(p, zero[bin], kWhole)) & 0x000fffffffffffffull;
+    }
+    // 2^f alone in units of 2^-shift, for sums within one bin
+    __device__ __forceinline__ uint64_t unit(double f, double in_vgpr_c4) const {
+        const double p = fma_scalar(fma_scalar(fma_scalar(f, in_vgpr_c4, c3), f, c2), f, c1);
+        return __builtin_bit_cast(uint64_t, fma_scalar(p, f, one)) & 0x000fffffffffffffull;
+    }
+    __device__ __forceinline__ uint64_t whole(uint64_t sum, int bin) const {  // such a sum, with the bin's factor
+        return bin ? uint64_t(__builtin_rint(double(sum) * (zero[-bin] * per_unit))) : sum;
     }
 };
 
-struct Shared {
-    uint64_t bin[kBins];
-    uint64_t list[kList];
-    uint64_t wave_sum[kWaves];
-    uint64_t lo, hi, before, total;
-    uint32_t count, found;
-    float f[kWaves];
-    float g[kWaves];
+// fp32 as a whole number that orders the same (-0.0 as +0.0), and back.
+__device__ __forceinline__ uint32_t ordered(float x) {
+    const uint32_t b = __float_as_uint(x + 0.0f);
+    return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+__device__ __forceinline__ float unordered(uint32_t o) {
+    return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
+}
+__device__ __forceinline__ float next_below(float x) { return unordered(ordered(x) - 1); }
+
+// Order of the elements as one 64-bit number, larger first: the logit, then the
+// index from the top down.
+__device__ __forceinline__ uint64_t order_key(float x, uint32_t idx) {
+    return (uint64_t(ordered(x)) << 32) | uint32_t(~idx);
+}
+__device__ __forceinline__ float key_value(uint64_t key) { return unordered(uint32_t(key >> 32)); }
+__device__ __forceinline__ uint32_t key_index(uint64_t key) { return ~uint32_t(key); }
+
+// What is kept by value: logits above `over`, and those equal to `equal` up to index `upto`.
+struct Cut {
+    float over = -INFINITY, equal = -INFINITY;
+    uint32_t upto = 0;
+
+    __device__ __forceinline__ bool operator()(float x, uint32_t i) const {
+        return (x > over) | ((x == equal) & (i <= upto));
+    }
+    __device__ void from_key(uint64_t key) { over = equal = key_value(key), upto = key_index(key); }
+    __device__ void from_value(float least) {  // and at or above `least`
+        if (least > over) over = next_below(least), equal = least, upto = 0xffffffffu;
+    }
 };
 
-__device__ __forceinline__ uint64_t shfl_up64(uint64_t v, int d) {
-    const uint32_t lo = __shfl_up(int(uint32_t(v)), d), hi = __shfl_up(int(uint32_t(v >> 32)), d);
-    return (uint64_t(hi) << 32) | lo;
+// ------------------------------------------------------------- block helpers
+
+struct Shared {
+    uint64_t bin[kSegs * kStride];
+    uint64_t list[kList];
+    uint64_t weight[kSmall];
+    double factor[kMass];
+    uint64_t seg[kSegs];
+    uint64_t wave_sum[kWaves];
+    uint64_t lo, hi, before;
+    uint32_t count, found;
+    float f[kWaves], g[kWaves];
+    float edge[2];
+};
+static_assert(kSearch <= kSegs * kStride, "find_first uses the histograms' memory");
+
+typedef unsigned long long ull;
+__device__ __forceinline__ void add64(uint64_t *p, uint64_t v) {
+    __hip_atomic_fetch_add(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
 }
+
 __device__ __forceinline__ uint64_t shfl_xor64(uint64_t v, int d) {
     const uint32_t lo = __shfl_xor(int(uint32_t(v)), d), hi = __shfl_xor(int(uint32_t(v >> 32)), d);
     return (uint64_t(hi) << 32) | lo;
 }
-__device__ __forceinline__ uint64_t wave_add(uint64_t v) {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) v += shfl_xor64(v, o);
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint64_t dpp64(uint64_t v) {  // 0 where the pattern has no source
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, int(uint32_t(v)), CTRL, ROWS, 0xf, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, int(uint32_t(v >> 32)), CTRL, ROWS, 0xf, false);
+    return (uint64_t(hi) << 32) | lo;
+}
+__device__ __forceinline__ uint64_t lane64(uint64_t v, int lane) {
+    const uint32_t lo = __builtin_amdgcn_readlane(int(uint32_t(v)), lane);
+    const uint32_t hi = __builtin_amdgcn_readlane(int(uint32_t(v >> 32)), lane);
+    return (uint64_t(hi) << 32) | lo;
+}
+// Running sum over the 16 lanes of each row, over the wave's 64 lanes (row shifts, then
+// the last lane of a row to the next one, of the first half to the second).
+__device__ __forceinline__ uint64_t row_scan(uint64_t v) {
+    v += dpp64<0x111, 0xf>(v);
+    v += dpp64<0x112, 0xf>(v);
+    v += dpp64<0x114, 0xf>(v);
+    v += dpp64<0x118, 0xf>(v);
     return v;
 }
-__device__ __forceinline__ uint64_t wave_scan(uint64_t v) {  // inclusive
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const uint64_t up = shfl_up64(v, o);
-        if (lane >= o) v += up;
-    }
+__device__ __forceinline__ uint64_t wave_scan(uint64_t v) {
+    v = row_scan(v);
+    v += dpp64<0x142, 0xa>(v);
+    v += dpp64<0x143, 0xc>(v);
     return v;
 }
+__device__ __forceinline__ uint64_t wave_add(uint64_t v) { return lane64(wave_scan(v), 63); }
 
-__device__ __forceinline__ void clear_bins(Shared &sh) {
-    for (int i = threadIdx.x; i < kBins; i += kThreads) sh.bin[i] = 0;
-    __syncthreads();
-}
-
-// The first bin at which the running sum reaches `target` (at least 1; a target
-// above the sum of all takes the last bin with anything): bin, sum before it.  All
-// threads call it after a barrier on the bins; ends with a barrier.
-__device__ __forceinline__ int find_bin(Shared &sh, uint64_t target, uint64_t *before, uint64_t *total) {
-    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-    const uint64_t b0 = sh.bin[2 * t], b1 = sh.bin[2 * t + 1];
-    const uint64_t own = b0 + b1;
+// Running sum over the block's threads: what comes before this thread's `own`,
+// and the sum of all.  Whatever all 16 waves do here costs 16 cycles an
+// instruction, so the waves' sums are scanned by 16 lanes of each.
+__device__ __forceinline__ uint64_t block_scan(Shared &sh, uint64_t own, uint64_t *all) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint64_t scan = wave_scan(own);
+    __syncthreads();
     if (lane == 63) sh.wave_sum[wave] = scan;
     __syncthreads();
-    uint64_t base = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-        const uint64_t s = sh.wave_sum[w];
-        if (w < wave) base += s;
-        all += s;
-    }
-    if (target > all) target = all;
-    const uint64_t pre = base + scan - own;
-    if (pre < target && pre + own >= target) {  // exactly one thread, where all > 0
-        const bool second = pre + b0 < target;
-        sh.found = 2 * t + (second ? 1 : 0);
+    const uint64_t waves = row_scan(sh.wave_sum[lane & 15]);
+    *all = lane64(waves, 15);
+    const uint64_t base = wave ? lane64(waves, (wave - 1) & 15) : 0;
+    return base + scan - own;
+}
+__device__ __forceinline__ uint64_t block_add(Shared &sh, uint64_t v) {
+    uint64_t all;
+    (void)block_scan(sh, v, &all);
+    return all;
+}
+
+// The least number of units that is `part` of `whole`, at least 1.
+__device__ __forceinline__ uint64_t at_least(float part, uint64_t whole) {
+    const uint64_t n = uint64_t(__builtin_ceil(double(part) * double(whole)));
+    return n < 1 ? 1 : (n > whole ? whole : n);
+}
+
+// The least number of units above u of `whole`.
+__device__ __forceinline__ uint64_t above(float u, uint64_t whole) {
+    if (!(u > 0.0f)) return 1;
+    if (u >= 1.0f) return whole;
+    const uint64_t n = uint64_t(double(u) * double(whole)) + 1;
+    return n > whole ? whole : n;
+}
+
+// The first bin at which the running sum of (b0, b1) -- this thread's bins 2t
+// and 2t + 1 -- reaches target(sum of all) (taken as at least 1 and at most the
+// sum).  Returns the bin; *before is the sum ahead of it.
+template <typename Target>
+__device__ __forceinline__ int find_bin(Shared &sh, uint64_t b0, uint64_t b1, Target target_of, uint64_t *before,
+                                        uint64_t *target) {
+    uint64_t all;
+    const uint64_t pre = block_scan(sh, b0 + b1, &all);
+    uint64_t t = target_of(all);
+    t = t > all ? all : t;
+    if (pre < t && pre + b0 + b1 >= t) {  // exactly one thread, where all > 0
+        const bool second = pre + b0 < t;
+        sh.found = 2 * threadIdx.x + (second ? 1 : 0);
         sh.before = second ? pre + b0 : pre;
     }
     __syncthreads();
     *before = sh.before;
-    *total = all;
-    return int(sh.found);
+    *target = t;
+    return all ? int(sh.found) : 0;
 }
 
-__device__ __forceinline__ uint64_t block_add(Shared &sh, uint64_t v) {
-    v = wave_add(v);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) sh.wave_sum[threadIdx.x >> 6] = v;
-    __syncthreads();
-    uint64_t all = 0;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) all += sh.wave_sum[w];
-    return all;
-}
-
-// The element, among those each(f) presents as f(key, weight) with lo <= key <=
-// hi, at which the weight summed from the largest key down first reaches
-// `target`.  Each round narrows [lo, hi] to one of 2048 bins of what is left.
+// The element, among those each(f) presents as f(key, weight), at which the
+// weight summed from the largest key down first reaches `target`.  Each round
+// narrows to one of 2048 bins of what is left.
 template <typename Each>
-__device__ __forceinline__ uint64_t find_first(Shared &sh, Each each, uint64_t target, uint64_t lo, uint64_t hi) {
+__device__ __forceinline__ uint64_t find_first(Shared &sh, Each each, uint64_t target) {
+    uint64_t lo = 0, hi = ~uint64_t(0);
     for (;;) {
         uint64_t least = ~uint64_t(0), most = 0;
         each([&](uint64_t key, uint64_t) {
@@ -187,10 +275,11 @@ __device__ __forceinline__ uint64_t find_first(Shared &sh, Each each, uint64_t t
         }
         __syncthreads();
         if (threadIdx.x == 0) sh.lo = ~uint64_t(0), sh.hi = 0;
-        clear_bins(sh);
+        for (int i = threadIdx.x; i < kSearch; i += kThreads) sh.bin[i] = 0;
+        __syncthreads();
         if ((threadIdx.x & 63) == 0) {
-            atomicMin(reinterpret_cast<unsigned long long *>(&sh.lo), (unsigned long long)least);
-            atomicMax(reinterpret_cast<unsigned long long *>(&sh.hi), (unsigned long long)most);
+            atomicMin(reinterpret_cast<ull *>(&sh.lo), ull(least));
+            atomicMax(reinterpret_cast<ull *>(&sh.hi), ull(most));
         }
         __syncthreads();
         least = sh.lo;
@@ -199,390 +288,618 @@ __device__ __forceinline__ uint64_t find_first(Shared &sh, Each each, uint64_t t
         const int bits = 64 - __builtin_clzll(most - least);
         const int drop = bits > 11 ? bits - 11 : 0;
         each([&](uint64_t key, uint64_t w) {
-            if (key >= least && key <= most)
-                atomicAdd(reinterpret_cast<unsigned long long *>(&sh.bin[(most - key) >> drop]), (unsigned long long)w);
+            if (key >= least && key <= most) add64(&sh.bin[(most - key) >> drop], w);
         });
         __syncthreads();
-        uint64_t before, total;
-        const uint64_t b = find_bin(sh, target, &before, &total);
-        if (total == 0) return most;
-        target = (target > total ? total : target) - before;
+        uint64_t before, t;
+        const uint64_t b = find_bin(sh, sh.bin[2 * threadIdx.x], sh.bin[2 * threadIdx.x + 1],
+                                    [&](uint64_t) { return target; }, &before, &t);
+        if (t == 0) return most;  // no weight at all
+        target = t - before;
         hi = most - (b << drop);
         const uint64_t width = (uint64_t(1) << drop) - 1;
         lo = hi - least > width ? hi - width : least;
     }
 }
 
-// A row: the first KEEP chunks of 16 bytes of each thread in registers, the
-// rest read again on each pass.  Chunk c of thread t holds elements
-// (c * 1024 + t) * E ..; elements past the row's end read as -inf.
-template <typename T, int KEEP>
+// ------------------------------------------------------------------- the row
+
+// Chunk c of thread t holds elements (c * 1024 + t) * E .. of the row; elements
+// past its end read as -inf.
+template <typename T>
 struct Row {
     static constexpr int E = 16 / sizeof(T);
     static constexpr int64_t kChunk = int64_t(kThreads) * E;
     const T *p;
     int64_t v;
-    u32x4 keep[KEEP];
+    int chunks, per;  // chunks of the row, and of each eighth of it
 
-    __device__ __forceinline__ u32x4 load(int64_t c) const {
+    __device__ Row(const SampleArgs &a, int64_t r) : p(static_cast<const T *>(a.logits) + r * a.ld), v(a.v) {
+        chunks = int((v + kChunk - 1) / kChunk);
+        per = (chunks + kSegs - 1) / kSegs;
+    }
+    __device__ __forceinline__ uint32_t index(int c) const { return uint32_t(c) * uint32_t(kChunk) + threadIdx.x * E; }
+    __device__ __forceinline__ int segment(uint32_t idx) const { return int(idx / uint32_t(kChunk)) / per; }
+    __device__ __forceinline__ u32x4 load_whole(int64_t c) const {
+        return load16(p + c * kChunk + int64_t(threadIdx.x) * E);
+    }
+    // The chunk that holds the row's last elements: 16 bytes that end with the
+    // row, moved down, -inf behind them.
+    __device__ __forceinline__ u32x4 load_last(int64_t c) const {
         const int64_t i = c * kChunk + int64_t(threadIdx.x) * E;
-        if (i + E <= v) return load16(p + i);
         constexpr uint32_t none = sizeof(T) == 4 ? 0xff800000u : (__is_same(T, bf16_t) ? 0xff80ff80u : 0xfc00fc00u);
         u32x4 x = {none, none, none, none};
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            if (i + e < v) {
+        if (i + E <= v) return load16(p + i);
+        if (i >= v) return x;
+        if (v >= E) x = load16(p + v - E);
+        const int n = v >= E ? int(i + E - v) : 0;  // elements to move down by
+        if (v < E)
+            for (int64_t j = v - 1; j >= 0; --j) {  // a row shorter than 16 bytes, from the last one down
                 if constexpr (sizeof(T) == 4) {
-                    x[e] = __float_as_uint(p[i + e]);
+                    x = u32x4{*reinterpret_cast<global_ptr<uint32_t>>((uintptr_t)(p + j)), x[0], x[1], x[2]};
                 } else {
-                    const uint32_t h = __builtin_bit_cast(uint16_t, p[i + e]);
-                    x[e >> 1] = (e & 1) ? (x[e >> 1] & 0xffffu) | (h << 16) : (x[e >> 1] & 0xffff0000u) | h;
+                    const uint32_t h = *reinterpret_cast<global_ptr<uint16_t>>((uintptr_t)(p + j));
+                    x = u32x4{(x[0] << 16) | h, (x[1] << 16) | (x[0] >> 16), (x[2] << 16) | (x[1] >> 16),
+                              (x[3] << 16) | (x[2] >> 16)};
                 }
             }
+        for (int j = 0; j < n; ++j) {
+            if constexpr (sizeof(T) == 4)
+                x = u32x4{x[1], x[2], x[3], none};
+            else
+                x = u32x4{(x[0] >> 16) | (x[1] << 16), (x[1] >> 16) | (x[2] << 16), (x[2] >> 16) | (x[3] << 16),
+                          (x[3] >> 16) | (none << 16)};
+        }
         return x;
     }
-    __device__ __forceinline__ int64_t chunks() const { return (v + kChunk - 1) / kChunk; }
-    __device__ __forceinline__ void fill() {
-        const int64_t n = chunks();
-#pragma unroll
-        for (int c = 0; c < KEEP; ++c)
-            if (c < n) keep[c] = load(c);
+    __device__ __forceinline__ u32x4 load(int64_t c) const {
+        return (c + 1) * kChunk <= v ? load_whole(c) : load_last(c);
     }
-    // f(16 bytes, chunk)
+    // f(16 bytes, chunk) over chunks c .. c1 - 1.  Two chunks are read while two are
+    // worked on: the registers are named apart, since handing a load on from one
+    // to the next would wait for it.
     template <typename F>
-    __device__ __forceinline__ void each_chunk(F f) const {
-        const int64_t n = chunks();
-#pragma unroll
-        for (int c = 0; c < KEEP; ++c)
-            if (c < n) f(keep[c], int64_t(c));
-        for (int64_t c = KEEP; c < n; ++c) f(load(c), c);
-    }
-    // f(value, index) of each element of a chunk; the loop is kept rolled over
-    // the words so that a pass over KEEP register chunks stays small
-    template <typename F>
-    __device__ __forceinline__ void each_in(u32x4 x, int64_t c, F f) const {
-        uint32_t i = uint32_t(c * kChunk + int64_t(threadIdx.x) * E);
+    __device__ __forceinline__ void each_chunk(F f, int c, int c1) const {
+        const int whole = min(c1, int(v / kChunk)), last = whole - 1;
+        if (c + 4 <= whole) {
+            u32x4 a0 = load_whole(c), a1 = load_whole(c + 1);
 #pragma unroll 1
-        for (int w = 0; w < 4; ++w) {
+            for (; c + 4 <= whole; c += 4) {
+                const u32x4 b0 = load_whole(c + 2), b1 = load_whole(c + 3);
+                f(a0, c);
+                f(a1, c + 1);
+                a0 = load_whole(min(c + 4, last));
+                a1 = load_whole(min(c + 5, last));
+                f(b0, c + 2);
+                f(b1, c + 3);
+            }
+        }
+#pragma unroll 1
+        for (; c < c1; ++c) f(load(c), c);
+    }
+    // f(value, index) of each element of chunks c .. c1 - 1, one chunk at a time: for
+    // the rarely taken paths, where small code matters more
+    template <typename F>
+    __device__ __forceinline__ void each(F f, int c, int c1) const {
+#pragma unroll 1
+        for (; c < c1; ++c) {
+            const u32x4 x = load(c);
+            const uint32_t i = index(c);
 #pragma unroll
-            for (int e = 0; e < E / 4; ++e) f(element<T>(x, e), i + e);
-            i += E / 4;
-            x = u32x4{x[1], x[2], x[3], x[0]};
+            for (int e = 0; e < E; ++e) f(element<T>(x, e), i + e);
         }
     }
     template <typename F>
     __device__ __forceinline__ void each(F f) const {
-        each_chunk([&](u32x4 x, int64_t c) { each_in(x, c, f); });
+        each(f, 0, chunks);
+    }
+    static __device__ __forceinline__ float largest(u32x4 x) {  // -inf for NaN
+        float m = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const float y = element<T>(x, e);
+            m = y > m ? y : m;
+        }
+        return m;
+    }
+    // The keys of the elements from `lo` on and below `hi` (hi = +inf: no end) to
+    // sh.list (up to kList; returns how many there are).
+    __device__ __forceinline__ uint32_t collect(Shared &sh, float lo, float hi) const {
+        if (threadIdx.x == 0) sh.count = 0;
+        __syncthreads();
+        each_chunk(
+            [&](u32x4 x, int c) {
+                if (!__any(largest(x) >= lo)) return;
+                const uint32_t i = index(c);
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const float y = element<T>(x, e);
+                    if (y >= lo && (y < hi || hi == INFINITY)) {
+                        const uint32_t at = atomicAdd(&sh.count, 1u);
+                        if (at < kList) sh.list[at] = order_key(y, i + e);
+                    }
+                }
+            },
+            0, chunks);
+        __syncthreads();
+        return sh.count;
     }
 };
 
-// Running sum reaches `part` of `whole` (a fraction in fp32): the least whole
-// number of units at or above it.
-__device__ __forceinline__ uint64_t at_least(float part, uint64_t whole) {
-    const double t = __builtin_ceil(double(part) * double(whole));
-    const uint64_t n = uint64_t(t);
-    return n < 1 ? 1 : (n > whole ? whole : n);
+// A row's settings.
+struct Settings {
+    float temperature, top_p, min_p, u;
+    int32_t top_k;
+    bool single;  // only the first token of the order is kept
+
+    __device__ Settings(const SampleArgs &a, int64_t r) {
+        temperature = a.set.temperatures ? a.set.temperatures[r] : a.set.temperature;
+        top_k = a.set.top_ks ? a.set.top_ks[r] : a.set.top_k;
+        top_p = a.set.top_ps ? a.set.top_ps[r] : a.set.top_p;
+        min_p = a.set.min_ps ? a.set.min_ps[r] : a.set.min_p;
+        u = a.u[r];
+        single = !(temperature > 0.0f) || top_k == 1 || !(top_p > 0.0f) || !(min_p <= 1.0f);
+        if (top_k < 0 || top_k >= a.v) top_k = 0;
+    }
+    // min-p as a logit: the smallest fp32 at or above top + T ln(min_p)
+    __device__ float least(float top) const {
+        if (!(min_p > 0.0f)) return -INFINITY;
+        const float x = __double2float_ru(double(top) + double(temperature) * log(double(min_p)));
+        return x <= top ? x : top;
+    }
+};
+
+struct Output {
+    int32_t *token;
+    float *prob;
+};
+
+__device__ __forceinline__ void write_row(Output out, int64_t r, uint32_t token, float prob) {
+    out.token[r] = int32_t(token);
+    if (out.prob) out.prob[r] = prob;
 }
 
-// Running sum exceeds u of `whole`.
-__device__ __forceinline__ uint64_t above(float u, uint64_t whole) {
-    if (!(u > 0.0f)) return 1;
-    if (u >= 1.0f) return whole;
-    const uint64_t n = uint64_t(double(u) * double(whole)) + 1;
-    return n > whole ? whole : n;
+// By the thread that found it.
+__device__ __forceinline__ void write_drawn(Output out, int64_t r, uint32_t token, float x, uint64_t sum,
+                                            const Weights &weight) {
+    int bin;
+    const double w = weight.power(x, &bin);
+    write_row(out, r, token, float(w * weight.zero[bin] / double(sum)));  // not rounded to whole units
 }
 
-template <typename T, int KEEP>
-__global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs args) {
-    __shared__ Shared sh;
-    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-    for (int64_t r = blockIdx.x; r < args.r; r += gridDim.x) {
-        __syncthreads();
-        Row<T, KEEP> row;
-        row.p = static_cast<const T *>(args.logits) + r * args.ld;
-        row.v = args.v;
-        row.fill();
-        const rt_sample_settings &set = args.set;
-        const float temperature = set.temperatures ? set.temperatures[r] : set.temperature;
-        const int32_t top_k = set.top_ks ? set.top_ks[r] : set.top_k;
-        const float top_p = set.top_ps ? set.top_ps[r] : set.top_p;
-        const float min_p = set.min_ps ? set.min_ps[r] : set.min_p;
-        const float u = args.u[r];
-
-        // the largest logit, and the smallest of the threads' largest
-        float own = -INFINITY;
-        row.each([&](float x, uint32_t) { own = fmaxf(own, x); });
-        float top = own, floor_ = own;
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) {
-            top = fmaxf(top, __shfl_xor(top, o));
-            floor_ = fminf(floor_, __shfl_xor(floor_, o));
-        }
-        if (lane == 0) sh.f[wave] = top, sh.g[wave] = floor_;
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-            top = fmaxf(top, sh.f[w]);
-            floor_ = fminf(floor_, sh.g[w]);
-        }
-        if (top == -INFINITY) {  // nothing to draw from
-            if (t == 0) {
-                args.out_token[r] = -1;
-                if (args.out_prob) args.out_prob[r] = 0.0f;
+// Sorts sh.list[0, n) down, zeros behind it to the next power of two from 128
+// on.  Pairs at distances up to 64 stay within one wave's 128 entries.
+__device__ __forceinline__ void sort_list(Shared &sh, uint32_t n) {
+    const uint32_t t = threadIdx.x;
+    uint32_t size = 128;
+    while (size < n) size *= 2;
+    for (uint32_t i = n + t; i < size; i += kThreads) sh.list[i] = 0;
+    __syncthreads();
+    for (uint32_t k = 2; k <= size; k *= 2) {
+        for (uint32_t j = k / 2; j > 0; j /= 2) {
+            if (t < size / 2) {
+                const uint32_t i = 2 * t - (t & (j - 1)), l = i + j;
+                const uint64_t a = sh.list[i], b = sh.list[l];
+                if ((a < b) == ((i & k) == 0)) sh.list[i] = b, sh.list[l] = a;
             }
-            continue;
+            if (j > 64 || (j == 1 && k >= 128 && k < size)) {
+                __syncthreads();
+            } else {
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                __builtin_amdgcn_wave_barrier();
+            }
         }
-        // settings that keep only the first token of the order
-        if (!(temperature > 0.0f) || top_k == 1 || !(top_p > 0.0f) || !(min_p <= 1.0f)) {
+    }
+    __syncthreads();
+}
+
+// The rest of a row whose kept elements are all in sh.list[0, n): top-k and
+// top-p (where on), min-p and the draw.  A barrier has followed the list.
+__device__ __forceinline__ void draw_from_list(Shared &sh, Output out, int64_t r, uint32_t n,
+                                               const Weights &weight, const Settings &set, float least) {
+    const uint32_t t = threadIdx.x;
+    const uint32_t limit = set.top_k ? min(n, uint32_t(set.top_k)) : n;
+    if (n <= kSmall) {
+        // eight neighbouring threads compare an element with all of them
+        const uint32_t i = t / 8, g = t % 8;
+        const bool mine = i < n && g == 0;
+        const uint64_t key = i < n ? sh.list[i] : 0;
+        const float x = i < n ? key_value(key) : -INFINITY;
+        const uint64_t w = weight(x);
+        if (mine) sh.weight[i] = w;
+        if (t == 0) sh.hi = 0;
+        __syncthreads();
+        uint32_t rank = 0;
+        uint64_t pre = 0;
+        for (uint32_t j = g; j < n; j += 8)
+            if (sh.list[j] > key) {
+                ++rank;
+                pre += sh.weight[j];
+            }
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) {
+            rank += uint32_t(__shfl_xor(int(rank), o));
+            pre += shfl_xor64(pre, o);
+        }
+        if (mine && rank == limit - 1) sh.before = pre + w;
+        __syncthreads();
+        bool kept = i < n && rank < limit && x >= least;
+        if (set.top_p < 1.0f) kept = kept && pre < at_least(set.top_p, sh.before);
+        if (mine) {
+            sh.weight[i] = kept ? w : 0;
+            if (kept) atomicMax(reinterpret_cast<ull *>(&sh.hi), ull(pre + w));  // kept ones are first in order
+        }
+        __syncthreads();
+        const uint64_t sum = sh.hi, aim = above(set.u, sum);
+        uint64_t run = 0;
+        for (uint32_t j = g; j < n; j += 8)
+            if (key_index(sh.list[j]) < key_index(key)) run += sh.weight[j];
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) run += shfl_xor64(run, o);
+        if (mine && kept && run < aim && run + w >= aim) write_drawn(out, r, key_index(key), x, sum, weight);
+        return;
+    }
+    sort_list(sh, n);
+    const uint64_t k0 = sh.list[2 * t], k1 = sh.list[2 * t + 1];
+    const float x0 = key_value(k0), x1 = key_value(k1);
+    bool keep0 = 2 * t < limit, keep1 = 2 * t + 1 < limit;
+    const uint64_t w0 = keep0 ? weight(x0) : 0, w1 = keep1 ? weight(x1) : 0;
+    if (set.top_p < 1.0f) {
+        uint64_t z;
+        const uint64_t pre = block_scan(sh, w0 + w1, &z);
+        const uint64_t aim = at_least(set.top_p, z);
+        keep0 = keep0 && pre < aim;
+        keep1 = keep1 && pre + w0 < aim;
+    }
+    keep0 = keep0 && x0 >= least;
+    keep1 = keep1 && x1 >= least;
+    const uint64_t sum = block_add(sh, (keep0 ? w0 : 0) + (keep1 ? w1 : 0));
+    const uint32_t token = ~uint32_t(find_first(
+        sh,
+        [&](auto f) {
+            if (keep0) f(uint64_t(uint32_t(k0)), w0);
+            if (keep1) f(uint64_t(uint32_t(k1)), w1);
+        },
+        above(set.u, sum)));
+    if (keep0 && key_index(k0) == token) write_drawn(out, r, token, x0, sum, weight);
+    if (keep1 && key_index(k1) == token) write_drawn(out, r, token, x1, sum, weight);
+}
+
+// The key in sh.list[0, n) at which the running weight reaches `target`.
+__device__ __forceinline__ uint64_t border_in_list(Shared &sh, uint32_t n, const Weights &weight, uint64_t target) {
+    sort_list(sh, n);
+    const uint32_t t = threadIdx.x;
+    const uint64_t k0 = sh.list[2 * t], k1 = sh.list[2 * t + 1];
+    const uint64_t w0 = 2 * t < n ? weight(key_value(k0)) : 0, w1 = 2 * t + 1 < n ? weight(key_value(k1)) : 0;
+    uint64_t before, aim;
+    const int b = find_bin(sh, w0, w1, [&](uint64_t) { return target; }, &before, &aim);
+    return sh.list[b];
+}
+
+// The draw once the eighths' kept weights are in sh.seg: the element of the
+// row at which the running weight of what `cut` keeps reaches above(u, sum).
+template <typename T>
+__device__ __forceinline__ void draw_from_row(Shared &sh, Output out, int64_t r, const Row<T> &row,
+                                              const Weights &weight, float u, const Cut &cut) {
+    uint64_t sum = 0;
+#pragma unroll
+    for (int s = 0; s < kSegs; ++s) sum += sh.seg[s];
+    uint64_t target = above(u, sum);
+    int seg = 0, last = 0;
+#pragma unroll
+    for (int s = 0; s < kSegs; ++s)
+        if (sh.seg[s]) last = s;
+    while (seg < last && sh.seg[seg] < target) target -= sh.seg[seg++];
+    const int end = min((seg + 1) * row.per, row.chunks);
+    for (int c = seg * row.per; c < end; ++c) {
+        const u32x4 x = row.load(c);
+        const uint32_t i = row.index(c);
+        constexpr int E = Row<T>::E;
+        uint64_t w[E], mine = 0;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const float y = element<T>(x, e);
+            w[e] = cut(y, i + e) ? weight(y) : 0;
+            mine += w[e];
+        }
+        uint64_t all;
+        uint64_t run = block_scan(sh, mine, &all);
+        if (all >= target || c + 1 == end) {
+            const uint64_t aim = min(target, all);
+            if (run < aim && run + mine >= aim) {
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    if (run < aim && run + w[e] >= aim)
+                        write_drawn(out, r, i + e, element<T>(x, e), sum, weight);
+                    run += w[e];
+                }
+            }
+            return;
+        }
+        target -= all;
+    }
+}
+
+// The rarely taken paths are functions of their own: inlined, they would cost
+// the others registers.  They take copies: what a call can change lives in memory.
+
+// The element of the row, from `lo` on and below `hi` (+inf: no end) and kept by
+// `cut`, at which the running weight (without `weigh`, their number) reaches `target`.
+template <typename T>
+__device__ __noinline__ uint64_t border_in_row(Shared &sh, Row<T> row, bool weigh, Weights weight, float lo, float hi,
+                                               Cut cut, uint64_t target) {
+    return find_first(
+        sh,
+        [&](auto f) {
+            row.each([&](float x, uint32_t i) {
+                if (x >= lo && (x < hi || hi == INFINITY) && cut(x, i)) f(order_key(x, i), weigh ? weight(x) : 1);
+            });
+        },
+        target);
+}
+
+// Any cut at all, where its elements do not fit the list: every element's weight again.
+template <typename T>
+__device__ __noinline__ void draw_by_cut(Shared &sh, Output out, int64_t r, Row<T> row, Weights weight, float u,
+                                         Cut cut) {
+    __syncthreads();
+    if (threadIdx.x < kSegs) sh.seg[threadIdx.x] = 0;
+    __syncthreads();
+    for (int s = 0; s < kSegs && s * row.per < row.chunks; ++s) {
+        uint64_t sum = 0;
+        row.each(
+            [&](float y, uint32_t i) {
+                if (cut(y, i)) sum += weight(y);
+            },
+            s * row.per, min((s + 1) * row.per, row.chunks));
+        sum = wave_add(sum);
+        if ((threadIdx.x & 63) == 0 && sum) add64(&sh.seg[s], sum);
+    }
+    __syncthreads();
+    draw_from_row(sh, out, r, row, weight, u, cut);
+}
+
+// A row whose largest logit is +inf: the infinite ones weigh the same, the rest nothing.
+template <typename T>
+__device__ __noinline__ void draw_infinite(Shared &sh, Output out, int64_t r, Row<T> row, Settings set) {
+    uint64_t n = 0;
+    row.each([&](float x, uint32_t) { n += x == INFINITY ? 1 : 0; });
+    n = block_add(sh, n);
+    if (set.top_k && n > uint64_t(set.top_k)) n = set.top_k;
+    if (set.top_p < 1.0f) n = at_least(set.top_p, n);
+    const uint64_t key = find_first(
+        sh,
+        [&](auto f) {
+            row.each([&](float x, uint32_t i) {
+                if (x == INFINITY) f(uint64_t(~i), uint64_t(1));
+            });
+        },
+        above(set.u, n));
+    if (threadIdx.x == 0) write_row(out, r, key_index(key), float(1.0 / double(n)));
+}
+
+// The smallest fp32 whose bin is at most b < kMass - 1, by one wave: 64 values
+// are tried at once.
+__device__ __forceinline__ float bin_edge(const Weights &weight, float top, int b) {
+    uint32_t lo = ordered(-__FLT_MAX__), hi = ordered(top);  // the bin of hi is at most b
+    while (lo < hi) {
+        const uint32_t step = (hi - lo) / 64 + 1, lane = threadIdx.x & 63;
+        const uint32_t x = hi - lo >= (lane + 1) * step ? hi - (lane + 1) * step : lo;
+        double f;
+        const bool in = hi - lo >= (lane + 1) * step && -weight.split(unordered(x), &f) <= b;
+        const uint32_t n = __popcll(__ballot(in));  // the first n values down from hi
+        const uint32_t down = hi - n * step;
+        lo = down - lo > step - 1 ? down - (step - 1) : lo;
+        hi = down;
+        if (step == 1) break;
+    }
+    return unordered(hi);
+}
+
+// The histograms of the weights of what `inside` keeps.
+template <typename T, typename Inside>
+__device__ __forceinline__ void mass_histogram(Shared &sh, const Row<T> &row, const Weights &weight, Inside inside) {
+    for (int i = threadIdx.x; i < kSegs * kStride; i += kThreads) sh.bin[i] = 0;
+    __syncthreads();
+    const int spread = kMass + (threadIdx.x & 63);
+    uint64_t *bins = sh.bin;
+    int left = row.per;
+    double c4 = weight.c4;
+    asm("" : "+v"(c4));  // one addend and one factor of an fma cannot both be scalar
+    row.each_chunk(
+        [&](u32x4 x, int c) {
+            const uint32_t i = row.index(c);
+#pragma unroll
+            for (int e = 0; e < Row<T>::E; ++e) {
+                const float y = element<T>(x, e);
+                double f;
+                const int b = -weight.split(y, &f);
+                const bool in = (b < kMass - 1) & inside(y, i + e);
+                add64(bins + (in ? b : spread), weight.unit(f, c4));
+            }
+            if (--left == 0) bins += kStride, left = row.per;
+        },
+        0, row.chunks);
+    __syncthreads();
+}
+
+// One row by one workgroup.
+template <typename T>
+__device__ __forceinline__ void sample_row(Shared &sh, const SampleArgs &args, int64_t r) {
+    const int t = threadIdx.x;
+    const Row<T> row(args, r);
+    const Settings set(args, r);
+    const Output out{args.out_token, args.out_prob};
+
+    // the largest logit, and the smallest finite one of the threads' largest
+    float own = -INFINITY;
+    row.each_chunk(
+        [&](u32x4 x, int) {
+            const float m = Row<T>::largest(x);
+            own = m > own ? m : own;
+        },
+        0, row.chunks);
+    float top = own, floor = own > -INFINITY ? own : INFINITY;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) {
+        top = fmaxf(top, __shfl_xor(top, o));
+        floor = fminf(floor, __shfl_xor(floor, o));
+    }
+    if ((t & 63) == 0) sh.f[t >> 6] = top, sh.g[t >> 6] = floor;
+    if (t == 0) sh.found = 0xffffffffu;
+    for (int i = t; i < kSearch; i += kThreads) sh.bin[i] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+        top = fmaxf(top, sh.f[w]);
+        floor = fminf(floor, sh.g[w]);
+    }
+    if (top == -INFINITY) {  // nothing to draw from
+        if (t == 0) write_row(out, r, 0xffffffffu, 0.0f);
+        return;
+    }
+    if (set.single) {  // the lowest index that holds it
+        if (__any(own == top)) {
             uint32_t first = 0xffffffffu;
             row.each([&](float x, uint32_t i) {
                 if (x >= top && i < first) first = i;
             });
+            if (first != 0xffffffffu) atomicMin(&sh.found, first);
+        }
+        __syncthreads();
+        if (t == 0) write_row(out, r, sh.found, 1.0f);
+        return;
+    }
+    if (top == INFINITY) return draw_infinite(sh, out, r, row, set);
+
+    const Weights weight{double(top), 1.4426950408889634 / kOctaves / double(set.temperature),
+                         (lds_doubles)(sh.factor + kMass - 1), args.c4, args.c3, args.c2, args.c1, args.one,
+                         args.per_unit};
+    const float least = set.least(top);
+    if (row.v <= kList) {
+        const uint32_t n = row.collect(sh, -__FLT_MAX__, INFINITY);
+        return draw_from_list(sh, out, r, n, weight, set, least);
+    }
+    Cut cut;
+    if (set.top_k) {
+        // k of the threads' largest logits reach the smallest value in the bin
+        // where their count reaches k, so at least k elements do
+        float from = -INFINITY;
+        if (set.top_k <= kThreads && floor < top) {
+            const float scale = fminf(float(kSearch - 1) / (top - floor), 1e30f);
+            const int b = own >= floor && own > -INFINITY
+                              ? min(int(fminf((top - own) * scale, float(kSearch))), kSearch - 1)
+                              : kSearch;
+            if (b < kSearch) add64(&sh.bin[b], 1);
+            __syncthreads();
+            uint64_t before, target, all = 0;
+            const int cutoff = find_bin(sh, sh.bin[2 * t], sh.bin[2 * t + 1],
+                                        [&](uint64_t sum) { all = sum; return uint64_t(set.top_k); }, &before, &target);
+            float m = b <= cutoff ? own : INFINITY;
 #pragma unroll
-            for (int o = 32; o > 0; o >>= 1) first = min(first, uint32_t(__shfl_xor(int(first), o)));
-            if (t == 0) sh.found = 0xffffffffu;
+            for (int o = 32; o > 0; o >>= 1) m = fminf(m, __shfl_xor(m, o));
+            if ((t & 63) == 0) sh.f[t >> 6] = m;
             __syncthreads();
-            if (lane == 0) atomicMin(&sh.found, first);
-            __syncthreads();
-            if (t == 0) {
-                args.out_token[r] = int32_t(sh.found);
-                if (args.out_prob) args.out_prob[r] = 1.0f;
-            }
-            continue;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) m = fminf(m, sh.f[w]);
+            if (all >= uint64_t(set.top_k)) from = m;
         }
-        const Weights weight{top, 1.4426950408889634 / double(temperature), args.shift};
-        // min-p as a logit: the smallest fp32 at or above top + T ln(min_p)
-        float least = -INFINITY;
-        if (min_p > 0.0f) {
-            const double cut = double(top) + double(temperature) * log(double(min_p));
-            least = __double2float_ru(cut);
-            if (!(least <= top)) least = top;
+        if (from > -INFINITY) {
+            const uint32_t n = row.collect(sh, from, INFINITY);
+            if (n <= kList) return draw_from_list(sh, out, r, n, weight, set, least);
         }
+        cut.from_key(border_in_row<T>(sh, row, false, weight, -__FLT_MAX__, INFINITY, cut, uint64_t(set.top_k)));
+        __syncthreads();
+    }
 
-        uint64_t border = 0;  // kept: keys at or above it (and logits at or above `least`)
-        bool listed = false;  // every kept element is in sh.list
-        uint32_t n_list = 0;
-        const bool k_on = top_k > 0 && top_k < args.v, p_on = top_p < 1.0f;
-
-        auto row_keys = [&](auto f) {
-            row.each([&](float x, uint32_t i) {
-                if (x >= -INFINITY && i < args.v) f(order_key(x, i), uint64_t(1));
-            });
-        };
-        if (k_on) {
-            // Bins over [low, top]; everything below goes to the last bin.  At
-            // least 1024 elements reach the smallest of the threads' largest.
-            float low = (top_k <= kThreads && floor_ > -INFINITY) ? floor_ : top - 22.0f * temperature;
-            const float scale = fminf(float(kBins - 2) / (top - low), 1e30f);
-            auto bin_of = [&](float x) {
-                if (x >= top) return 0;
-                return x >= low ? min(int(fminf((top - x) * scale, float(kBins))), kBins - 2) : kBins - 1;
-            };
-            clear_bins(sh);
-            uint32_t below = 0;
-            row.each([&](float x, uint32_t i) {
-                if (x >= low)
-                    atomicAdd(reinterpret_cast<unsigned long long *>(&sh.bin[bin_of(x)]), 1ull);
-                else
-                    below += i < args.v ? 1 : 0;  // NaN and -inf, too: the last of the order
-            });
-            const uint64_t under = wave_add(below);
-            if (lane == 0) atomicAdd(reinterpret_cast<unsigned long long *>(&sh.bin[kBins - 1]), (unsigned long long)under);
-            if (t == 0) sh.count = 0;
-            __syncthreads();
-            uint64_t before, total;
-            const int b = find_bin(sh, uint64_t(top_k), &before, &total);
-            const uint64_t upto = before + sh.bin[b];
-            if (b == kBins - 1) {
-                border = find_first(sh, row_keys, uint64_t(top_k), 0, ~uint64_t(0));
-            } else if (upto <= kList) {
-                row.each([&](float x, uint32_t i) {
-                    if (x >= low && bin_of(x) <= b) {
-                        const uint32_t at = atomicAdd(&sh.count, 1u);
-                        if (at < kList) sh.list[at] = order_key(x, i);  // always: `upto` of them
-                    }
-                });
-                __syncthreads();
-                listed = true;
-                n_list = uint32_t(upto);
-                border = find_first(
-                    sh,
-                    [&](auto f) {
-                        for (uint32_t j = t; j < n_list; j += kThreads) f(sh.list[j], uint64_t(1));
-                    },
-                    uint64_t(top_k), 0, ~uint64_t(0));
-            } else {
-                border = find_first(
-                    sh,
-                    [&](auto f) {
-                        row.each([&](float x, uint32_t i) {
-                            if (x >= low && bin_of(x) == b) f(order_key(x, i), uint64_t(1));
-                        });
-                    },
-                    uint64_t(top_k) - before, 0, ~uint64_t(0));
-            }
+    const bool cut_k = set.top_k != 0;
+    if (cut_k)
+        mass_histogram(sh, row, weight, cut);
+    else
+        mass_histogram(sh, row, weight, [](float, uint32_t) { return true; });
+    // the bin that the border cuts: top-p's, or min-p's where it comes first
+    uint64_t before = 0, target = 0;
+    int b = kMass;
+    if (set.top_p < 1.0f) {
+        uint64_t b0 = 0, b1 = 0;
+        if (2 * t < kMass - 1) {
+#pragma unroll
+            for (int s = 0; s < kSegs; ++s) b0 += sh.bin[s * kStride + 2 * t], b1 += sh.bin[s * kStride + 2 * t + 1];
+            b0 = weight.whole(b0, 2 * t);
+            b1 = weight.whole(b1, 2 * t + 1);
         }
-        auto list_weights = [&](auto f) {
-            for (uint32_t j = t; j < n_list; j += kThreads) {
-                const uint64_t key = sh.list[j];
-                if (key >= border) f(key, weight(key_value(key)));
-            }
-        };
-        if (p_on && listed) {
-            uint64_t z = 0;
-            list_weights([&](uint64_t, uint64_t w) { z += w; });
-            z = block_add(sh, z);
-            border = find_first(sh, list_weights, at_least(top_p, z), 0, ~uint64_t(0));
-        } else if (p_on) {
-            // 64 bins an octave of weight, 32 octaves; lighter ones in the last bin
-            const float scale = float(fmin(64.0 * weight.rate, 1e30));
-            auto bin_of = [&](float x) {
-                return x >= top ? 0 : int(fminf((top - x) * scale, float(kBins - 1)));
-            };
-            const float border_value = border ? key_value(border) : -INFINITY;
-            auto inside = [&](float x, uint32_t i) {
-                return x > border_value || (x == border_value && order_key(x, i) >= border && x > -INFINITY);
-            };
-            clear_bins(sh);
-            uint64_t light = 0;
-            row.each([&](float x, uint32_t i) {
-                if (inside(x, i)) {
-                    const int b = bin_of(x);
-                    const uint64_t w = weight(x);
-                    if (b < kBins - 1)
-                        atomicAdd(reinterpret_cast<unsigned long long *>(&sh.bin[b]), (unsigned long long)w);
-                    else
-                        light += w;
-                }
-            });
-            light = wave_add(light);
-            if (lane == 0) atomicAdd(reinterpret_cast<unsigned long long *>(&sh.bin[kBins - 1]), (unsigned long long)light);
-            if (t == 0) sh.count = 0, sh.total = 0;
-            __syncthreads();
-            uint64_t before, z;
-            (void)find_bin(sh, 1, &before, &z);
-            const uint64_t target = at_least(top_p, z);
-            const int b = find_bin(sh, target, &before, &z);
-            row.each([&](float x, uint32_t i) {
-                if (inside(x, i) && bin_of(x) == b) {
-                    const uint32_t at = atomicAdd(&sh.count, 1u);
-                    if (at < kList) sh.list[at] = order_key(x, i);
-                }
-            });
-            __syncthreads();
-            const uint32_t n = sh.count;
-            if (n <= kList)
-                border = find_first(
-                    sh,
-                    [&](auto f) {
-                        for (uint32_t j = t; j < n; j += kThreads) f(sh.list[j], weight(key_value(sh.list[j])));
-                    },
-                    target - before, 0, ~uint64_t(0));
-            else
-                border = find_first(
-                    sh,
-                    [&](auto f) {
-                        row.each([&](float x, uint32_t i) {
-                            if (inside(x, i) && bin_of(x) == b) f(order_key(x, i), weight(x));
-                        });
-                    },
-                    target - before, 0, ~uint64_t(0));
-        }
-
-        // the draw
-        uint32_t token;
-        float value;
-        uint64_t sum;
-        if (listed) {
-            auto by_index = [&](auto f) {
-                for (uint32_t j = t; j < n_list; j += kThreads) {
-                    const uint64_t key = sh.list[j];
-                    const float x = key_value(key);
-                    if (key >= border && x >= least) f(uint64_t(uint32_t(key)), weight(x));
-                }
-            };
-            uint64_t s = 0;
-            by_index([&](uint64_t, uint64_t w) { s += w; });
-            sum = block_add(sh, s);
-            token = ~uint32_t(find_first(sh, by_index, above(u, sum), 0, ~uint64_t(0)));
-        } else {
-            const float border_value = border ? key_value(border) : -INFINITY;
-            auto kept = [&](float x, uint32_t i) {
-                return x >= least && (x > border_value || (x == border_value && order_key(x, i) >= border)) &&
-                       x > -INFINITY;
-            };
-            const int64_t chunks = row.chunks(), per = (chunks + kSegs - 1) / kSegs;
-            clear_bins(sh);
-            uint64_t s = 0;
-            row.each_chunk([&](u32x4 x, int64_t c) {
-                row.each_in(x, c, [&](float y, uint32_t i) {
-                    if (kept(y, i)) s += weight(y);
-                });
-                if ((c + 1) % per == 0 || c + 1 == chunks) {
-                    const uint64_t all = wave_add(s);
-                    if (lane == 0 && all)
-                        atomicAdd(reinterpret_cast<unsigned long long *>(&sh.bin[c / per]), (unsigned long long)all);
-                    s = 0;
-                }
-            });
-            __syncthreads();
-            uint64_t before;
-            (void)find_bin(sh, 1, &before, &sum);
-            uint64_t target = above(u, sum);
-            const int64_t seg = find_bin(sh, target, &before, &sum);
-            target -= before;
-            token = 0;
-            const int64_t last = min((seg + 1) * per, chunks);
-            for (int64_t c = seg * per; c < last; ++c) {
-                // this chunk again: a bin per 64 / 128 ... threads' own elements
-                const u32x4 x = row.load(c);
-                uint64_t mine = 0;
-                row.each_in(x, c, [&](float y, uint32_t i) {
-                    if (kept(y, i)) mine += weight(y);
-                });
-                const uint64_t scan = wave_scan(mine);
-                __syncthreads();
-                if (lane == 63) sh.wave_sum[wave] = scan;
-                __syncthreads();
-                uint64_t base = 0, all = 0;
-                for (int w = 0; w < kWaves; ++w) {
-                    if (w < wave) base += sh.wave_sum[w];
-                    all += sh.wave_sum[w];
-                }
-                if (all >= target) {
-                    uint64_t run = base + scan - mine;
-                    if (run < target && run + mine >= target)
-                        row.each_in(x, c, [&](float y, uint32_t i) {
-                            if (kept(y, i)) {
-                                const uint64_t w = weight(y);
-                                if (run < target && run + w >= target) sh.found = i;
-                                run += w;
-                            }
-                        });
-                    __syncthreads();
-                    token = sh.found;
-                    break;
-                }
-                target -= all;
-            }
-        }
-        if (t == 0) {
-            token = min(token, uint32_t(args.v - 1));
-            args.out_token[r] = int32_t(token);
-            if (args.out_prob) {
-                value = static_cast<float>(static_cast<const T *>(args.logits)[r * args.ld + token]);
-                const double w = value >= top ? __builtin_ldexp(1.0, args.shift) : weight.power(value);
-                args.out_prob[r] = float(w / double(sum));
-            }
+        b = find_bin(sh, b0, b1, [&](uint64_t all) { return at_least(set.top_p, all); }, &before, &target);
+    }
+    bool by_p = b < kMass;
+    if (least > -INFINITY) {
+        double f;
+        const int l = -weight.split(least, &f);
+        if (l < b) by_p = false, b = l;
+    }
+    if (b >= kMass - 1) b = kMass;  // the border lies among elements without weight, or there is none
+    // the weights kept whole, by eighth
+    if (t < kSegs) sh.seg[t] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int s = 0; s < kSegs; ++s) {
+        uint64_t sum = 0;
+        if (2 * t < min(b, kMass - 1)) sum = weight.whole(sh.bin[s * kStride + 2 * t], 2 * t);
+        if (2 * t + 1 < min(b, kMass - 1)) sum += weight.whole(sh.bin[s * kStride + 2 * t + 1], 2 * t + 1);
+        if (__any(sum != 0)) {
+            sum = wave_add(sum);
+            if ((t & 63) == 0) add64(&sh.seg[s], sum);
         }
     }
+    if (b < kMass) {
+        if (t < 128) {
+            const int at = b - (t >> 6);
+            const float e = at >= 0 ? bin_edge(weight, top, at) : INFINITY;
+            if ((t & 63) == 0) sh.edge[t >> 6] = e;
+        }
+        __syncthreads();
+        const float lo = sh.edge[0], hi = sh.edge[1];
+        const uint32_t n = cut_k ? kList + 1 : row.collect(sh, lo, hi);
+        if (n > kList) {
+            if (by_p)
+                cut.from_key(border_in_row<T>(sh, row, true, weight, lo, hi, cut, target - before));
+            cut.from_value(least);
+            return draw_by_cut(sh, out, r, row, weight, set.u, cut);
+        }
+        if (by_p) cut.from_key(border_in_list(sh, n, weight, target - before));
+        cut.from_value(least);
+        for (uint32_t j = t; j < n; j += kThreads) {
+            const uint64_t key = sh.list[j];
+            if (cut(key_value(key), key_index(key)))
+                add64(&sh.seg[row.segment(key_index(key))], weight(key_value(key)));
+        }
+    }
+    __syncthreads();
+    draw_from_row(sh, out, r, row, weight, set.u, cut);
+}
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void row_kernel(SampleArgs args, int64_t first) {
+    extern __shared__ __align__(16) char memory[];
+    Shared &sh = *reinterpret_cast<Shared *>(memory);
+    for (int b = threadIdx.x; b < kMass; b += kThreads)
+        sh.factor[kMass - 1 - b] =
+            b < kMass - 1 ? __builtin_ldexp(exp2(double(b % kPerOctave) / -kPerOctave), args.shift - b / kPerOctave) : 0.0;
+    sample_row<T>(sh, args, first + blockIdx.x);  // its first barrier is ahead of the factors' first use
 }
 
 template <typename T>
 hipError_t launch(const SampleArgs &a, hipStream_t s) {
-    const unsigned grid = unsigned(a.r < (1 << 20) ? a.r : (1 << 20));
-    sample_kernel<T, 2><<<grid, kThreads, 0, s>>>(a);
-    return hipGetLastError();
+    hipError_t err = hipFuncSetAttribute(reinterpret_cast<const void *>(row_kernel<T>),
+                                         hipFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(Shared)));
+    // a workgroup per row: a loop over rows in the kernel would keep what the
+    // passes have in common in registers across all of them
+    constexpr int64_t kMost = 1 << 20;
+    for (int64_t first = 0; first < a.r && err == hipSuccess; first += kMost) {
+        const int64_t rows = a.r - first < kMost ? a.r - first : kMost;
+        row_kernel<T><<<unsigned(rows), kThreads, sizeof(Shared), s>>>(a, first);
+        err = hipGetLastError();
+    }
+    return err;
 }
 
 }  // namespace
@@ -597,7 +914,10 @@ extern "C" rt_status rt_sample_rows(const void *logits, int32_t dtype, int64_t r
     int log2v = 0;
     while ((int64_t(1) << log2v) < v) ++log2v;
     const int shift = 62 - log2v < 46 ? 62 - log2v : 46;
-    const rt::SampleArgs a{logits, r, v, ld, u, *settings, out_token, out_prob, shift};
+    const double unit = double(int64_t(1) << shift);
+    const rt::SampleArgs a{logits,         r,         v,         ld,         u,           *settings,
+                           out_token,      out_prob,  shift,     rt::kC4 * unit, rt::kC3 * unit, rt::kC2 * unit,
+                           rt::kC1 * unit, unit + rt::kWhole, 1.0 / unit};
     hipStream_t s = static_cast<hipStream_t>(stream);
     hipError_t err;
     switch (dtype) {
