@@ -82,6 +82,25 @@ __device__ __forceinline__ double fma_scalar(double a, double b, double c) {
     return d;
 }
 
+// The same for four independent sums at a time: an instruction that needs the
+// one before it right after an asm block waits a cycle more (s_nop).
+struct Four {
+    double v[4];
+};
+__device__ __forceinline__ void fma_four(Four &d, const Four &a, const Four &b, double c) {
+    asm("v_fma_f64 %0, %4, %8, %12\n\tv_fma_f64 %1, %5, %9, %12\n\t"
+        "v_fma_f64 %2, %6, %10, %12\n\tv_fma_f64 %3, %7, %11, %12"
+        : "=&v"(d.v[0]), "=&v"(d.v[1]), "=&v"(d.v[2]), "=&v"(d.v[3])
+        : "v"(a.v[0]), "v"(a.v[1]), "v"(a.v[2]), "v"(a.v[3]), "v"(b.v[0]), "v"(b.v[1]), "v"(b.v[2]), "v"(b.v[3]),
+          "s"(c));
+}
+__device__ __forceinline__ void fma_four(Four &d, const Four &a, double b, double c) {  // b in vector registers
+    asm("v_fma_f64 %0, %4, %8, %9\n\tv_fma_f64 %1, %5, %8, %9\n\t"
+        "v_fma_f64 %2, %6, %8, %9\n\tv_fma_f64 %3, %7, %8, %9"
+        : "=&v"(d.v[0]), "=&v"(d.v[1]), "=&v"(d.v[2]), "=&v"(d.v[3])
+        : "v"(a.v[0]), "v"(a.v[1]), "v"(a.v[2]), "v"(a.v[3]), "v"(b), "s"(c));
+}
+
 struct Weights {
     double top, rate;  // rate = log2(e) / (47 T)
     lds_doubles zero;  // the factor of bin 0; bin b's is at zero[-b]
@@ -103,10 +122,26 @@ struct Weights {
         const double p = power(x, &bin);
         return __builtin_bit_cast(uint64_t, fma_scalar(p, zero[bin], kWhole)) & 0x000fffffffffffffull;
     }
-    // 2^f alone in units of 2^-shift, for sums within one bin
-    __device__ __forceinline__ uint64_t unit(double f, double in_vgpr_c4) const {
-        const double p = fma_scalar(fma_scalar(fma_scalar(f, in_vgpr_c4, c3), f, c2), f, c1);
-        return __builtin_bit_cast(uint64_t, fma_scalar(p, f, one)) & 0x000fffffffffffffull;
+    // For four elements: -bin, and 2^f alone in units of 2^-shift, for sums
+    // within one bin.
+    __device__ __forceinline__ void units(const float *x, int *bin, uint64_t *unit) const {
+        double octaves = kOctaves, lead = c4;
+        asm("" : "+v"(octaves), "+v"(lead));  // an fma reads at most one scalar pair
+        Four sigma, m, f, p;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sigma.v[e] = fmin(fmax(fma(double(x[e]) - top, rate, 1.0), 0.0), 1.0);
+        fma_four(m, sigma, octaves, kRound - kOctaves);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            bin[e] = int(uint32_t(__builtin_bit_cast(uint64_t, m.v[e])));
+            f.v[e] = fma(sigma.v[e], octaves, (kRound - kOctaves) - m.v[e]);
+        }
+        fma_four(p, f, lead, c3);
+        fma_four(p, p, f, c2);
+        fma_four(p, p, f, c1);
+        fma_four(p, p, f, one);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) unit[e] = __builtin_bit_cast(uint64_t, p.v[e]) & 0x000fffffffffffffull;
     }
     __device__ __forceinline__ uint64_t whole(uint64_t sum, int bin) const {  // such a sum, with the bin's factor
         return bin ? uint64_t(__builtin_rint(double(sum) * (zero[-bin] * per_unit))) : sum;
@@ -139,8 +174,8 @@ struct Cut {
     __device__ __forceinline__ bool operator()(float x, uint32_t i) const {
         return (x > over) | ((x == equal) & (i <= upto));
     }
-    __device__ void from_key(uint64_t key) { over = equal = key_value(key), upto = key_index(key); }
-    __device__ void from_value(float least) {  // and at or above `least`
+    __device__ __forceinline__ void from_key(uint64_t key) { over = equal = key_value(key), upto = key_index(key); }
+    __device__ __forceinline__ void from_value(float least) {  // and at or above `least`
         if (least > over) over = next_below(least), equal = least, upto = 0xffffffffu;
     }
 };
@@ -159,7 +194,7 @@ struct Shared {
     float f[kWaves], g[kWaves];
     float edge[2];
 };
-static_assert(kSearch <= kSegs * kStride, "find_first uses the histograms' memory");
+static_assert(kSearch + kThreads / 2 <= kSegs * kStride, "find_first uses the histograms' memory");
 
 typedef unsigned long long ull;
 __device__ __forceinline__ void add64(uint64_t *p, uint64_t v) {
@@ -176,11 +211,42 @@ __device__ __forceinline__ uint64_t dpp64(uint64_t v) {  // 0 where the pattern 
     const uint32_t hi = __builtin_amdgcn_update_dpp(0, int(uint32_t(v >> 32)), CTRL, ROWS, 0xf, false);
     return (uint64_t(hi) << 32) | lo;
 }
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp32(float v, float none) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(none), __float_as_int(v), CTRL, ROWS, 0xf, false));
+}
+// Largest and smallest of the wave's 64 lanes (no NaN).
+__device__ __forceinline__ float wave_max(float v) {
+    v = fmaxf(v, dpp32<0x111, 0xf>(v, -INFINITY));
+    v = fmaxf(v, dpp32<0x112, 0xf>(v, -INFINITY));
+    v = fmaxf(v, dpp32<0x114, 0xf>(v, -INFINITY));
+    v = fmaxf(v, dpp32<0x118, 0xf>(v, -INFINITY));
+    v = fmaxf(v, dpp32<0x142, 0xa>(v, -INFINITY));
+    v = fmaxf(v, dpp32<0x143, 0xc>(v, -INFINITY));
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+__device__ __forceinline__ float wave_min(float v) { return -wave_max(-v); }
+
 __device__ __forceinline__ uint64_t lane64(uint64_t v, int lane) {
     const uint32_t lo = __builtin_amdgcn_readlane(int(uint32_t(v)), lane);
     const uint32_t hi = __builtin_amdgcn_readlane(int(uint32_t(v >> 32)), lane);
     return (uint64_t(hi) << 32) | lo;
 }
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint64_t max_dpp64(uint64_t v) {
+    const uint64_t o = dpp64<CTRL, ROWS>(v);
+    return o > v ? o : v;
+}
+__device__ __forceinline__ uint64_t wave_max64(uint64_t v) {
+    v = max_dpp64<0x111, 0xf>(v);
+    v = max_dpp64<0x112, 0xf>(v);
+    v = max_dpp64<0x114, 0xf>(v);
+    v = max_dpp64<0x118, 0xf>(v);
+    v = max_dpp64<0x142, 0xa>(v);
+    v = max_dpp64<0x143, 0xc>(v);
+    return lane64(v, 63);
+}
+
 // Running sum over the 16 lanes of each row, over the wave's 64 lanes (row shifts, then
 // the last lane of a row to the next one, of the first half to the second).
 __device__ __forceinline__ uint64_t row_scan(uint64_t v) {
@@ -314,19 +380,21 @@ struct Row {
     int64_t v;
     int chunks, per;  // chunks of the row, and of each eighth of it
 
-    __device__ Row(const SampleArgs &a, int64_t r) : p(static_cast<const T *>(a.logits) + r * a.ld), v(a.v) {
+    __device__ __forceinline__ Row(const SampleArgs &a, int64_t r) : p(static_cast<const T *>(a.logits) + r * a.ld), v(a.v) {
         chunks = int((v + kChunk - 1) / kChunk);
         per = (chunks + kSegs - 1) / kSegs;
     }
-    __device__ __forceinline__ uint32_t index(int c) const { return uint32_t(c) * uint32_t(kChunk) + threadIdx.x * E; }
+    __device__ __forceinline__ uint32_t index(int c, uint32_t t = threadIdx.x) const {
+        return uint32_t(c) * uint32_t(kChunk) + t * E;
+    }
     __device__ __forceinline__ int segment(uint32_t idx) const { return int(idx / uint32_t(kChunk)) / per; }
-    __device__ __forceinline__ u32x4 load_whole(int64_t c) const {
-        return load16(p + c * kChunk + int64_t(threadIdx.x) * E);
+    __device__ __forceinline__ u32x4 load_whole(int64_t c, uint32_t t = threadIdx.x) const {
+        return load16(p + c * kChunk + int64_t(t) * E);
     }
     // The chunk that holds the row's last elements: 16 bytes that end with the
     // row, moved down, -inf behind them.
-    __device__ __forceinline__ u32x4 load_last(int64_t c) const {
-        const int64_t i = c * kChunk + int64_t(threadIdx.x) * E;
+    __device__ __forceinline__ u32x4 load_last(int64_t c, uint32_t t = threadIdx.x) const {
+        const int64_t i = c * kChunk + int64_t(t) * E;
         constexpr uint32_t none = sizeof(T) == 4 ? 0xff800000u : (__is_same(T, bf16_t) ? 0xff80ff80u : 0xfc00fc00u);
         u32x4 x = {none, none, none, none};
         if (i + E <= v) return load16(p + i);
@@ -352,8 +420,8 @@ struct Row {
         }
         return x;
     }
-    __device__ __forceinline__ u32x4 load(int64_t c) const {
-        return (c + 1) * kChunk <= v ? load_whole(c) : load_last(c);
+    __device__ __forceinline__ u32x4 load(int64_t c, uint32_t t = threadIdx.x) const {
+        return (c + 1) * kChunk <= v ? load_whole(c, t) : load_last(c, t);
     }
     // f(16 bytes, chunk) over chunks c .. c1 - 1.  Two chunks are read while two are
     // worked on: the registers are named apart, since handing a load on from one
@@ -402,25 +470,61 @@ struct Row {
         }
         return m;
     }
-    // The keys of the elements from `lo` on and below `hi` (hi = +inf: no end) to
-    // sh.list (up to kList; returns how many there are).
+    // The keys of the 16 bytes' elements from `lo` on and below `hi` (+inf: no end)
+    // to sh.list, up to kList of them; sh.count counts them all.
+    static __device__ __forceinline__ void take(Shared &sh, u32x4 x, uint32_t i, float lo, float hi) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const float y = element<T>(x, e);
+            const bool in = (y >= lo) & (y < hi);
+            if (__any(in)) {
+                if (in) {
+                    const uint32_t at = atomicAdd(&sh.count, 1u);
+                    if (at < kList) sh.list[at] = order_key(y, i + e);
+                }
+            }
+        }
+    }
+    // The whole row's; returns sh.count.  FEW: most 16 bytes hold none, and one test
+    // of their largest settles them.
+    template <bool FEW>
     __device__ __forceinline__ uint32_t collect(Shared &sh, float lo, float hi) const {
         if (threadIdx.x == 0) sh.count = 0;
         __syncthreads();
         each_chunk(
             [&](u32x4 x, int c) {
-                if (!__any(largest(x) >= lo)) return;
-                const uint32_t i = index(c);
+                if (FEW && !__any(largest(x) >= lo)) return;
+                take(sh, x, index(c), lo, hi);
+            },
+            0, chunks);
+        __syncthreads();
+        return sh.count;
+    }
+    // The same without an end, where few threads' largest logit `own` reaches lo:
+    // the waves take those threads' places one by one, a chunk a lane.
+    __device__ __forceinline__ uint32_t collect_from(Shared &sh, float lo, float own) const {
+        uint32_t *threads = reinterpret_cast<uint32_t *>(sh.bin + kSearch);
+        __syncthreads();  // sh.found has been read
+        if (threadIdx.x == 0) sh.count = 0, sh.found = 0;
+        __syncthreads();
+        if (own >= lo) threads[atomicAdd(&sh.found, 1u)] = threadIdx.x;
+        __syncthreads();
+        const uint32_t n = sh.found;
+        for (uint32_t h = threadIdx.x >> 6; h < n; h += kWaves) {
+            const uint32_t t = threads[h];
+            for (int c = threadIdx.x & 63; c < chunks; c += 64) {
+                const u32x4 x = load(c, t);
+                const uint32_t i = index(c, t);
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
                     const float y = element<T>(x, e);
-                    if (y >= lo && (y < hi || hi == INFINITY)) {
+                    if (y >= lo) {
                         const uint32_t at = atomicAdd(&sh.count, 1u);
                         if (at < kList) sh.list[at] = order_key(y, i + e);
                     }
                 }
-            },
-            0, chunks);
+            }
+        }
         __syncthreads();
         return sh.count;
     }
@@ -432,17 +536,21 @@ struct Settings {
     int32_t top_k;
     bool single;  // only the first token of the order is kept
 
-    __device__ Settings(const SampleArgs &a, int64_t r) {
-        temperature = a.set.temperatures ? a.set.temperatures[r] : a.set.temperature;
-        top_k = a.set.top_ks ? a.set.top_ks[r] : a.set.top_k;
-        top_p = a.set.top_ps ? a.set.top_ps[r] : a.set.top_p;
-        min_p = a.set.min_ps ? a.set.min_ps[r] : a.set.min_p;
+    __device__ __forceinline__ Settings(const SampleArgs &a, int64_t r) {
+        temperature = a.set.temperature;
+        top_k = a.set.top_k;
+        top_p = a.set.top_p;
+        min_p = a.set.min_p;
+        if (a.set.temperatures) temperature = a.set.temperatures[r];
+        if (a.set.top_ks) top_k = a.set.top_ks[r];
+        if (a.set.top_ps) top_p = a.set.top_ps[r];
+        if (a.set.min_ps) min_p = a.set.min_ps[r];
         u = a.u[r];
         single = !(temperature > 0.0f) || top_k == 1 || !(top_p > 0.0f) || !(min_p <= 1.0f);
         if (top_k < 0 || top_k >= a.v) top_k = 0;
     }
     // min-p as a logit: the smallest fp32 at or above top + T ln(min_p)
-    __device__ float least(float top) const {
+    __device__ __forceinline__ float least(float top) const {
         if (!(min_p > 0.0f)) return -INFINITY;
         const float x = __double2float_ru(double(top) + double(temperature) * log(double(min_p)));
         return x <= top ? x : top;
@@ -465,6 +573,84 @@ __device__ __forceinline__ void write_drawn(Output out, int64_t r, uint32_t toke
     int bin;
     const double w = weight.power(x, &bin);
     write_row(out, r, token, float(w * weight.zero[bin] / double(sum)));  // not rounded to whole units
+}
+
+// find_first for at most two elements a thread (weight 0: none), `n` in all, with
+// keys in [least, most].  Once at most kSmall are left, eight threads compare
+// one of them with all.  Returns true to the one thread that holds the element
+// (the last one, where the weights do not reach the target; key 0, where there
+// are none).  Uses sh.list and sh.bin.
+struct Pair {
+    uint64_t key[2], weight[2];
+};
+__device__ __forceinline__ bool find_in_pairs(Shared &sh, Pair p, uint32_t n, uint64_t least, uint64_t most,
+                                              uint64_t target, uint64_t *found) {
+    const int t = threadIdx.x, lane = t & 63;
+    for (;;) {
+        if (n > kSmall) {
+            __syncthreads();
+            for (int i = t; i < kSearch; i += kThreads) sh.bin[i] = 0;
+            __syncthreads();
+            const int bits = 64 - __builtin_clzll(most - least);  // more than one key: they differ
+            const int drop = bits > 11 ? bits - 11 : 0;
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (p.weight[e]) add64(&sh.bin[(most - p.key[e]) >> drop], p.weight[e]);
+            __syncthreads();
+            uint64_t before, aim;
+            const uint64_t b = find_bin(sh, sh.bin[2 * t], sh.bin[2 * t + 1], [&](uint64_t) { return target; },
+                                        &before, &aim);
+            target = aim - before;
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (p.weight[e] && ((most - p.key[e]) >> drop) != b) p.weight[e] = 0;
+        }
+        // what is left: how many, between which keys, and the first kSmall side by side
+        __syncthreads();
+        if (t == 0) sh.lo = ~uint64_t(0), sh.hi = 0, sh.count = 0;
+        __syncthreads();
+        const uint64_t m0 = __ballot(p.weight[0] != 0), m1 = __ballot(p.weight[1] != 0);
+        if (m0 | m1) {
+            uint64_t low = ~uint64_t(0), high = 0;
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (p.weight[e]) {
+                    low = p.key[e] < low ? p.key[e] : low;
+                    high = p.key[e] > high ? p.key[e] : high;
+                }
+            low = ~wave_max64(~low);
+            high = wave_max64(high);
+            uint32_t at = 0;
+            if (lane == 0) {
+                atomicMin(reinterpret_cast<ull *>(&sh.lo), ull(low));
+                atomicMax(reinterpret_cast<ull *>(&sh.hi), ull(high));
+                at = atomicAdd(&sh.count, uint32_t(__popcll(m0) + __popcll(m1)));
+            }
+            at = __builtin_amdgcn_readfirstlane(at);
+            const uint64_t below = (uint64_t(1) << lane) - 1;
+            const uint32_t a0 = at + __popcll(m0 & below), a1 = at + __popcll(m0) + __popcll(m1 & below);
+            if (p.weight[0] && a0 < kSmall) sh.list[a0] = p.key[0], sh.weight[a0] = p.weight[0];
+            if (p.weight[1] && a1 < kSmall) sh.list[a1] = p.key[1], sh.weight[a1] = p.weight[1];
+        }
+        __syncthreads();
+        n = sh.count;
+        least = sh.lo;
+        most = sh.hi;
+        *found = 0;
+        if (n == 0) return t == 0;
+        if (n <= kSmall) {
+            const uint32_t i = t / 8, g = t % 8;
+            if (i >= n) return false;
+            const uint64_t key = sh.list[i], w = sh.weight[i];
+            uint64_t run = 0;
+            for (uint32_t j = g; j < n; j += 8)
+                if (sh.list[j] > key) run += sh.weight[j];
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) run += shfl_xor64(run, o);
+            *found = key;
+            return g == 0 && run < target && (run + w >= target || key == least);
+        }
+    }
 }
 
 // Sorts sh.list[0, n) down, zeros behind it to the next power of two from 128
@@ -495,8 +681,10 @@ __device__ __forceinline__ void sort_list(Shared &sh, uint32_t n) {
 
 // The rest of a row whose kept elements are all in sh.list[0, n): top-k and
 // top-p (where on), min-p and the draw.  A barrier has followed the list.
-__device__ __forceinline__ void draw_from_list(Shared &sh, Output out, int64_t r, uint32_t n,
-                                               const Weights &weight, const Settings &set, float least) {
+// row_value(i) is logit i.
+template <typename Value>
+__device__ __forceinline__ void draw_from_list(Shared &sh, Output out, int64_t r, uint32_t n, const Weights &weight,
+                                               const Settings &set, float least, uint32_t v, Value row_value) {
     const uint32_t t = threadIdx.x;
     const uint32_t limit = set.top_k ? min(n, uint32_t(set.top_k)) : n;
     if (n <= kSmall) {
@@ -554,26 +742,25 @@ __device__ __forceinline__ void draw_from_list(Shared &sh, Output out, int64_t r
     keep0 = keep0 && x0 >= least;
     keep1 = keep1 && x1 >= least;
     const uint64_t sum = block_add(sh, (keep0 ? w0 : 0) + (keep1 ? w1 : 0));
-    const uint32_t token = ~uint32_t(find_first(
-        sh,
-        [&](auto f) {
-            if (keep0) f(uint64_t(uint32_t(k0)), w0);
-            if (keep1) f(uint64_t(uint32_t(k1)), w1);
-        },
-        above(set.u, sum)));
-    if (keep0 && key_index(k0) == token) write_drawn(out, r, token, x0, sum, weight);
-    if (keep1 && key_index(k1) == token) write_drawn(out, r, token, x1, sum, weight);
+    const uint64_t i0 = uint32_t(k0), i1 = uint32_t(k1);  // by index, the lowest first
+    uint64_t key;
+    if (find_in_pairs(sh, Pair{{i0, i1}, {keep0 ? w0 : 0, keep1 ? w1 : 0}}, n, ~(v - 1), 0xffffffffu,
+                      above(set.u, sum), &key)) {
+        const uint32_t token = key_index(key);
+        write_drawn(out, r, token, row_value(token), sum, weight);
+    }
 }
 
-// The key in sh.list[0, n) at which the running weight reaches `target`.
-__device__ __forceinline__ uint64_t border_in_list(Shared &sh, uint32_t n, const Weights &weight, uint64_t target) {
-    sort_list(sh, n);
-    const uint32_t t = threadIdx.x;
-    const uint64_t k0 = sh.list[2 * t], k1 = sh.list[2 * t + 1];
-    const uint64_t w0 = 2 * t < n ? weight(key_value(k0)) : 0, w1 = 2 * t + 1 < n ? weight(key_value(k1)) : 0;
-    uint64_t before, aim;
-    const int b = find_bin(sh, w0, w1, [&](uint64_t) { return target; }, &before, &aim);
-    return sh.list[b];
+// sh.list[0, n), two elements a thread, with their weights.
+__device__ __forceinline__ Pair pairs_of_list(Shared &sh, uint32_t n, const Weights &weight) {
+    Pair p;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const uint32_t j = threadIdx.x + e * kThreads;
+        p.key[e] = j < n ? sh.list[j] : 0;
+        p.weight[e] = j < n ? weight(key_value(p.key[e])) : 0;
+    }
+    return p;
 }
 
 // The draw once the eighths' kept weights are in sh.seg: the element of the
@@ -626,13 +813,13 @@ __device__ __forceinline__ void draw_from_row(Shared &sh, Output out, int64_t r,
 // The element of the row, from `lo` on and below `hi` (+inf: no end) and kept by
 // `cut`, at which the running weight (without `weigh`, their number) reaches `target`.
 template <typename T>
-__device__ __noinline__ uint64_t border_in_row(Shared &sh, Row<T> row, bool weigh, Weights weight, float lo, float hi,
+__device__ __forceinline__ uint64_t border_in_row(Shared &sh, Row<T> row, bool weigh, Weights weight, float lo, float hi,
                                                Cut cut, uint64_t target) {
     return find_first(
         sh,
         [&](auto f) {
             row.each([&](float x, uint32_t i) {
-                if (x >= lo && (x < hi || hi == INFINITY) && cut(x, i)) f(order_key(x, i), weigh ? weight(x) : 1);
+                if (x >= lo && x < hi && cut(x, i)) f(order_key(x, i), weigh ? weight(x) : 1);
             });
         },
         target);
@@ -640,7 +827,7 @@ __device__ __noinline__ uint64_t border_in_row(Shared &sh, Row<T> row, bool weig
 
 // Any cut at all, where its elements do not fit the list: every element's weight again.
 template <typename T>
-__device__ __noinline__ void draw_by_cut(Shared &sh, Output out, int64_t r, Row<T> row, Weights weight, float u,
+__device__ __forceinline__ void draw_by_cut(Shared &sh, Output out, int64_t r, Row<T> row, Weights weight, float u,
                                          Cut cut) {
     __syncthreads();
     if (threadIdx.x < kSegs) sh.seg[threadIdx.x] = 0;
@@ -661,7 +848,7 @@ __device__ __noinline__ void draw_by_cut(Shared &sh, Output out, int64_t r, Row<
 
 // A row whose largest logit is +inf: the infinite ones weigh the same, the rest nothing.
 template <typename T>
-__device__ __noinline__ void draw_infinite(Shared &sh, Output out, int64_t r, Row<T> row, Settings set) {
+__device__ __forceinline__ void draw_infinite(Shared &sh, Output out, int64_t r, Row<T> row, Settings set) {
     uint64_t n = 0;
     row.each([&](float x, uint32_t) { n += x == INFINITY ? 1 : 0; });
     n = block_add(sh, n);
@@ -701,21 +888,26 @@ template <typename T, typename Inside>
 __device__ __forceinline__ void mass_histogram(Shared &sh, const Row<T> &row, const Weights &weight, Inside inside) {
     for (int i = threadIdx.x; i < kSegs * kStride; i += kThreads) sh.bin[i] = 0;
     __syncthreads();
-    const int spread = kMass + (threadIdx.x & 63);
-    uint64_t *bins = sh.bin;
+    // bin b of a segment is at [kMass - 1 - b]
+    const int spread = kMass - (kMass - 1) + int(threadIdx.x & 63);
+    uint64_t *bins = sh.bin + kMass - 1;
     int left = row.per;
-    double c4 = weight.c4;
-    asm("" : "+v"(c4));  // one addend and one factor of an fma cannot both be scalar
     row.each_chunk(
         [&](u32x4 x, int c) {
             const uint32_t i = row.index(c);
 #pragma unroll
-            for (int e = 0; e < Row<T>::E; ++e) {
-                const float y = element<T>(x, e);
-                double f;
-                const int b = -weight.split(y, &f);
-                const bool in = (b < kMass - 1) & inside(y, i + e);
-                add64(bins + (in ? b : spread), weight.unit(f, c4));
+            for (int h = 0; h < Row<T>::E / 4; ++h) {
+                float y[4];
+                int b[4];
+                uint64_t unit[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] = element<T>(x, h * 4 + e);
+                weight.units(y, b, unit);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const bool in = (b[e] > 1 - kMass) & inside(y[e], i + h * 4 + e);
+                    add64(bins + (in ? b[e] : spread), unit[e]);
+                }
             }
             if (--left == 0) bins += kStride, left = row.per;
         },
@@ -740,20 +932,14 @@ __device__ __forceinline__ void sample_row(Shared &sh, const SampleArgs &args, i
         },
         0, row.chunks);
     float top = own, floor = own > -INFINITY ? own : INFINITY;
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) {
-        top = fmaxf(top, __shfl_xor(top, o));
-        floor = fminf(floor, __shfl_xor(floor, o));
-    }
+    top = wave_max(top);
+    floor = wave_min(floor);
     if ((t & 63) == 0) sh.f[t >> 6] = top, sh.g[t >> 6] = floor;
     if (t == 0) sh.found = 0xffffffffu;
     for (int i = t; i < kSearch; i += kThreads) sh.bin[i] = 0;
     __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-        top = fmaxf(top, sh.f[w]);
-        floor = fminf(floor, sh.g[w]);
-    }
+    top = wave_max(sh.f[t & (kWaves - 1)]);
+    floor = wave_min(sh.g[t & (kWaves - 1)]);
     if (top == -INFINITY) {  // nothing to draw from
         if (t == 0) write_row(out, r, 0xffffffffu, 0.0f);
         return;
@@ -776,37 +962,40 @@ __device__ __forceinline__ void sample_row(Shared &sh, const SampleArgs &args, i
                          (lds_doubles)(sh.factor + kMass - 1), args.c4, args.c3, args.c2, args.c1, args.one,
                          args.per_unit};
     const float least = set.least(top);
+    const auto value = [&](uint32_t i) { return static_cast<float>(row.p[i]); };
     if (row.v <= kList) {
-        const uint32_t n = row.collect(sh, -__FLT_MAX__, INFINITY);
-        return draw_from_list(sh, out, r, n, weight, set, least);
+        const uint32_t n = row.template collect<false>(sh, -__FLT_MAX__, INFINITY);
+        return draw_from_list(sh, out, r, n, weight, set, least, uint32_t(row.v), value);
     }
     Cut cut;
     if (set.top_k) {
-        // k of the threads' largest logits reach the smallest value in the bin
-        // where their count reaches k, so at least k elements do
-        float from = -INFINITY;
+        // A value that at least k elements reach, and few more: the lower edge of the
+        // bin where the count of the threads' largest logits reaches k, or, for
+        // many, that of the 16-byte chunks' largest: of 1024 (or v / 8), one thread (or
+        // chunk) seldom holds two of the first k.
+        const bool by_thread = set.top_k <= kThreads / 4;
+        const float scale = fminf(float(kSearch - 1) / (top - floor), 1e30f);
         if (set.top_k <= kThreads && floor < top) {
-            const float scale = fminf(float(kSearch - 1) / (top - floor), 1e30f);
-            const int b = own >= floor && own > -INFINITY
-                              ? min(int(fminf((top - own) * scale, float(kSearch))), kSearch - 1)
-                              : kSearch;
-            if (b < kSearch) add64(&sh.bin[b], 1);
+            auto count = [&](float x) {
+                if (x >= floor && x > -INFINITY) 
+                    add64(&sh.bin[min(int(fminf((top - x) * scale, float(kSearch))), kSearch - 1)], 1);
+            };
+            if (by_thread)
+                count(own);
+            else
+                row.each_chunk([&](u32x4 x, int) { count(Row<T>::largest(x)); }, 0, row.chunks);
             __syncthreads();
             uint64_t before, target, all = 0;
-            const int cutoff = find_bin(sh, sh.bin[2 * t], sh.bin[2 * t + 1],
-                                        [&](uint64_t sum) { all = sum; return uint64_t(set.top_k); }, &before, &target);
-            float m = b <= cutoff ? own : INFINITY;
-#pragma unroll
-            for (int o = 32; o > 0; o >>= 1) m = fminf(m, __shfl_xor(m, o));
-            if ((t & 63) == 0) sh.f[t >> 6] = m;
-            __syncthreads();
-#pragma unroll
-            for (int w = 0; w < kWaves; ++w) m = fminf(m, sh.f[w]);
-            if (all >= uint64_t(set.top_k)) from = m;
-        }
-        if (from > -INFINITY) {
-            const uint32_t n = row.collect(sh, from, INFINITY);
-            if (n <= kList) return draw_from_list(sh, out, r, n, weight, set, least);
+            const int last = find_bin(sh, sh.bin[2 * t], sh.bin[2 * t + 1],
+                                      [&](uint64_t sum) { all = sum; return uint64_t(set.top_k); }, &before, &target);
+            if (all >= uint64_t(set.top_k)) {
+                // the roundings of a bin are far below 2^-20 of its distance and 2^-22 of top
+                const float edge = top - float(last + 1) / scale * 1.000001f - fabsf(top) * 2.4e-7f;
+                const float from = fmaxf(edge, floor);
+                const uint32_t n = by_thread ? row.collect_from(sh, from, own)
+                                             : row.template collect<true>(sh, from, INFINITY);
+                if (n <= kList) return draw_from_list(sh, out, r, n, weight, set, least, uint32_t(row.v), value);
+            }
         }
         cut.from_key(border_in_row<T>(sh, row, false, weight, -__FLT_MAX__, INFINITY, cut, uint64_t(set.top_k)));
         __syncthreads();
@@ -824,7 +1013,7 @@ __device__ __forceinline__ void sample_row(Shared &sh, const SampleArgs &args, i
         uint64_t b0 = 0, b1 = 0;
         if (2 * t < kMass - 1) {
 #pragma unroll
-            for (int s = 0; s < kSegs; ++s) b0 += sh.bin[s * kStride + 2 * t], b1 += sh.bin[s * kStride + 2 * t + 1];
+            for (int s = 0; s < kSegs; ++s) b0 += sh.bin[s * kStride + kMass - 1 - 2 * t], b1 += sh.bin[s * kStride + kMass - 2 - 2 * t];
             b0 = weight.whole(b0, 2 * t);
             b1 = weight.whole(b1, 2 * t + 1);
         }
@@ -837,14 +1026,20 @@ __device__ __forceinline__ void sample_row(Shared &sh, const SampleArgs &args, i
         if (l < b) by_p = false, b = l;
     }
     if (b >= kMass - 1) b = kMass;  // the border lies among elements without weight, or there is none
-    // the weights kept whole, by eighth
+    // about how many elements bin b holds, and the weights kept whole, by eighth
+    uint64_t in_bin = 0;
+    if (b < kMass) {
+#pragma unroll
+        for (int s = 0; s < kSegs; ++s) in_bin += sh.bin[s * kStride + kMass - 1 - b];
+        in_bin >>= args.shift;
+    }
     if (t < kSegs) sh.seg[t] = 0;
     __syncthreads();
 #pragma unroll
     for (int s = 0; s < kSegs; ++s) {
         uint64_t sum = 0;
-        if (2 * t < min(b, kMass - 1)) sum = weight.whole(sh.bin[s * kStride + 2 * t], 2 * t);
-        if (2 * t + 1 < min(b, kMass - 1)) sum += weight.whole(sh.bin[s * kStride + 2 * t + 1], 2 * t + 1);
+        if (2 * t < min(b, kMass - 1)) sum = weight.whole(sh.bin[s * kStride + kMass - 1 - 2 * t], 2 * t);
+        if (2 * t + 1 < min(b, kMass - 1)) sum += weight.whole(sh.bin[s * kStride + kMass - 2 - 2 * t], 2 * t + 1);
         if (__any(sum != 0)) {
             sum = wave_add(sum);
             if ((t & 63) == 0) add64(&sh.seg[s], sum);
@@ -858,20 +1053,30 @@ __device__ __forceinline__ void sample_row(Shared &sh, const SampleArgs &args, i
         }
         __syncthreads();
         const float lo = sh.edge[0], hi = sh.edge[1];
-        const uint32_t n = cut_k ? kList + 1 : row.collect(sh, lo, hi);
+        const uint32_t n = cut_k ? kList + 1
+                           : in_bin <= 256 ? row.template collect<true>(sh, lo, hi)
+                                           : row.template collect<false>(sh, lo, hi);
         if (n > kList) {
             if (by_p)
                 cut.from_key(border_in_row<T>(sh, row, true, weight, lo, hi, cut, target - before));
             cut.from_value(least);
             return draw_by_cut(sh, out, r, row, weight, set.u, cut);
         }
-        if (by_p) cut.from_key(border_in_list(sh, n, weight, target - before));
-        cut.from_value(least);
-        for (uint32_t j = t; j < n; j += kThreads) {
-            const uint64_t key = sh.list[j];
-            if (cut(key_value(key), key_index(key)))
-                add64(&sh.seg[row.segment(key_index(key))], weight(key_value(key)));
+        const Pair p = pairs_of_list(sh, n, weight);
+        if (by_p) {
+            uint64_t key;
+            if (find_in_pairs(sh, p, n, uint64_t(ordered(lo)) << 32, (uint64_t(ordered(fminf(hi, top))) << 32) | 0xffffffffu,
+                              target - before, &key))
+                sh.before = key;
+            __syncthreads();
+            key = sh.before;
+            if (key) cut.from_key(key);  // else the bin's weights all round to 0: what it holds cannot be drawn
         }
+        cut.from_value(least);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            if (p.weight[e] && cut(key_value(p.key[e]), key_index(p.key[e])))
+                add64(&sh.seg[row.segment(key_index(p.key[e]))], p.weight[e]);
     }
     __syncthreads();
     draw_from_row(sh, out, r, row, weight, set.u, cut);
