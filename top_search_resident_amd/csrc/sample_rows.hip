@@ -39,6 +39,7 @@ constexpr int kList = 2048;   // candidates kept in LDS
 constexpr int kSmall = 128;   // lists up to here are settled by comparing all pairs
 constexpr int kSegs = 8;      // parts of a row with a histogram each
 constexpr int kSearch = 2048; // bins of find_first, two per thread
+constexpr int kPlaces = 4096; // 16-byte places that hold candidates
 
 struct SampleArgs {
     const void *logits;
@@ -194,7 +195,7 @@ struct Shared {
     float f[kWaves], g[kWaves];
     float edge[2];
 };
-static_assert(kSearch + kThreads / 2 <= kSegs * kStride, "find_first uses the histograms' memory");
+static_assert(kSearch <= kSegs * kStride && kPlaces / 2 <= kSegs * kStride, "find_first uses the histograms' memory");
 
 typedef unsigned long long ull;
 __device__ __forceinline__ void add64(uint64_t *p, uint64_t v) {
@@ -470,41 +471,56 @@ struct Row {
         }
         return m;
     }
-    // The keys of the 16 bytes' elements from `lo` on and below `hi` (+inf: no end)
-    // to sh.list, up to kList of them; sh.count counts them all.
+    // The keys of the 16 bytes' elements from `lo` on and below `hi` (+inf: no end; no
+    // logit is infinite here) to sh.list, up to kList of them; sh.count counts them all.
     static __device__ __forceinline__ void take(Shared &sh, u32x4 x, uint32_t i, float lo, float hi) {
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             const float y = element<T>(x, e);
-            const bool in = (y >= lo) & (y < hi);
-            if (__any(in)) {
-                if (in) {
-                    const uint32_t at = atomicAdd(&sh.count, 1u);
-                    if (at < kList) sh.list[at] = order_key(y, i + e);
-                }
+            if (y >= lo && y < hi) {
+                const uint32_t at = atomicAdd(&sh.count, 1u);
+                if (at < kList) sh.list[at] = order_key(y, i + e);
             }
         }
     }
-    // The whole row's; returns sh.count.  FEW: most 16 bytes hold none, and one test
-    // of their largest settles them.
-    template <bool FEW>
+    // The whole row's; returns sh.count.  First the places of the 16 bytes that hold
+    // any (one note for a wave's, where noting each element would cost more than
+    // reading those again), then their elements, a thread each.  `END`: hi counts.
+    template <bool END>
     __device__ __forceinline__ uint32_t collect(Shared &sh, float lo, float hi) const {
-        if (threadIdx.x == 0) sh.count = 0;
+        uint32_t *places = reinterpret_cast<uint32_t *>(sh.bin);
+        __syncthreads();  // sh.bin, sh.found and sh.count have been read
+        if (threadIdx.x == 0) sh.count = 0, sh.found = 0;
         __syncthreads();
         each_chunk(
             [&](u32x4 x, int c) {
-                if (FEW && !__any(largest(x) >= lo)) return;
-                take(sh, x, index(c), lo, hi);
+                bool any = false;
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const float y = element<T>(x, e);
+                    any |= END ? (y >= lo) & (y < hi) : y >= lo;
+                }
+                if (any) {
+                    const uint32_t at = atomicAdd(&sh.found, 1u);
+                    if (at < kPlaces) places[at] = uint32_t(c) * kThreads + threadIdx.x;
+                }
             },
             0, chunks);
+        __syncthreads();
+        const uint32_t n = sh.found;
+        if (n > kPlaces) return kList + 1;
+        for (uint32_t j = threadIdx.x; j < n; j += kThreads) {
+            const uint32_t c = places[j] / kThreads, t = places[j] % kThreads;
+            take(sh, load(c, t), index(c, t), lo, END ? hi : INFINITY);
+        }
         __syncthreads();
         return sh.count;
     }
     // The same without an end, where few threads' largest logit `own` reaches lo:
     // the waves take those threads' places one by one, a chunk a lane.
     __device__ __forceinline__ uint32_t collect_from(Shared &sh, float lo, float own) const {
-        uint32_t *threads = reinterpret_cast<uint32_t *>(sh.bin + kSearch);
-        __syncthreads();  // sh.found has been read
+        uint32_t *threads = reinterpret_cast<uint32_t *>(sh.bin);
+        __syncthreads();  // sh.bin, sh.found and sh.count have been read
         if (threadIdx.x == 0) sh.count = 0, sh.found = 0;
         __syncthreads();
         if (own >= lo) threads[atomicAdd(&sh.found, 1u)] = threadIdx.x;
@@ -513,16 +529,7 @@ struct Row {
         for (uint32_t h = threadIdx.x >> 6; h < n; h += kWaves) {
             const uint32_t t = threads[h];
             for (int c = threadIdx.x & 63; c < chunks; c += 64) {
-                const u32x4 x = load(c, t);
-                const uint32_t i = index(c, t);
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const float y = element<T>(x, e);
-                    if (y >= lo) {
-                        const uint32_t at = atomicAdd(&sh.count, 1u);
-                        if (at < kList) sh.list[at] = order_key(y, i + e);
-                    }
-                }
+                take(sh, load(c, t), index(c, t), lo, INFINITY);
             }
         }
         __syncthreads();
@@ -865,16 +872,24 @@ __device__ __forceinline__ void draw_infinite(Shared &sh, Output out, int64_t r,
     if (threadIdx.x == 0) write_row(out, r, key_index(key), float(1.0 / double(n)));
 }
 
-// The smallest fp32 whose bin is at most b < kMass - 1, by one wave: 64 values
-// are tried at once.
+// The smallest fp32 whose bin is at most b < kMass - 1, by one wave, which tries
+// 64 values at once: those around where the bin's edge lies in real numbers,
+// and, where that fails (next to zero fp32 is finer than the 64-bit logits'
+// rounding), a 64th of what is left at a time.
 __device__ __forceinline__ float bin_edge(const Weights &weight, float top, int b) {
+    const uint32_t lane = threadIdx.x & 63;
+    double f;
     uint32_t lo = ordered(-__FLT_MAX__), hi = ordered(top);  // the bin of hi is at most b
+    const uint32_t near = ordered(float(weight.top - (b + 0.5) / (kPerOctave * kOctaves) / weight.rate));
+    if (near > lo + 64 && near < hi - 64) {
+        const uint64_t in = __ballot(-weight.split(unordered(near - 32 + lane), &f) <= b);
+        if (in != 0 && !(in & 1)) return unordered(near - 32 + uint32_t(__builtin_ctzll(in)));
+    }
     while (lo < hi) {
-        const uint32_t step = (hi - lo) / 64 + 1, lane = threadIdx.x & 63;
-        const uint32_t x = hi - lo >= (lane + 1) * step ? hi - (lane + 1) * step : lo;
-        double f;
-        const bool in = hi - lo >= (lane + 1) * step && -weight.split(unordered(x), &f) <= b;
-        const uint32_t n = __popcll(__ballot(in));  // the first n values down from hi
+        const uint32_t step = (hi - lo) / 64 + 1;
+        const bool inside = hi - lo >= (lane + 1) * step;
+        const uint32_t x = inside ? hi - (lane + 1) * step : lo;
+        const uint32_t n = __popcll(__ballot(inside && -weight.split(unordered(x), &f) <= b));  // the first n down from hi
         const uint32_t down = hi - n * step;
         lo = down - lo > step - 1 ? down - (step - 1) : lo;
         hi = down;
@@ -923,15 +938,21 @@ __device__ __forceinline__ void sample_row(Shared &sh, const SampleArgs &args, i
     const Settings set(args, r);
     const Output out{args.out_token, args.out_prob};
 
-    // the largest logit, and the smallest finite one of the threads' largest
-    float own = -INFINITY;
+    // the largest logit, and the smallest finite one
+    // of the threads' largest, each over every fourth of its chunks
+    float own[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
     row.each_chunk(
-        [&](u32x4 x, int) {
+        [&](u32x4 x, int c) {
             const float m = Row<T>::largest(x);
-            own = m > own ? m : own;
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+                if ((c & 3) == g) own[g] = m > own[g] ? m : own[g];
         },
         0, row.chunks);
-    float top = own, floor = own > -INFINITY ? own : INFINITY;
+    const float mine = fmaxf(fmaxf(own[0], own[1]), fmaxf(own[2], own[3]));
+    float top = mine, floor = INFINITY;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) floor = fminf(floor, own[g] > -INFINITY ? own[g] : INFINITY);
     top = wave_max(top);
     floor = wave_min(floor);
     if ((t & 63) == 0) sh.f[t >> 6] = top, sh.g[t >> 6] = floor;
@@ -945,7 +966,7 @@ __device__ __forceinline__ void sample_row(Shared &sh, const SampleArgs &args, i
         return;
     }
     if (set.single) {  // the lowest index that holds it
-        if (__any(own == top)) {
+        if (__any(mine == top)) {
             uint32_t first = 0xffffffffu;
             row.each([&](float x, uint32_t i) {
                 if (x >= top && i < first) first = i;
@@ -970,20 +991,14 @@ __device__ __forceinline__ void sample_row(Shared &sh, const SampleArgs &args, i
     Cut cut;
     if (set.top_k) {
         // A value that at least k elements reach, and few more: the lower edge of the
-        // bin where the count of the threads' largest logits reaches k, or, for
-        // many, that of the 16-byte chunks' largest: of 1024 (or v / 8), one thread (or
-        // chunk) seldom holds two of the first k.
-        const bool by_thread = set.top_k <= kThreads / 4;
+        // bin where the count of those 4096 largest logits reaches k (of 4096, one
+        // seldom hides another of the first k).
         const float scale = fminf(float(kSearch - 1) / (top - floor), 1e30f);
         if (set.top_k <= kThreads && floor < top) {
-            auto count = [&](float x) {
-                if (x >= floor && x > -INFINITY) 
-                    add64(&sh.bin[min(int(fminf((top - x) * scale, float(kSearch))), kSearch - 1)], 1);
-            };
-            if (by_thread)
-                count(own);
-            else
-                row.each_chunk([&](u32x4 x, int) { count(Row<T>::largest(x)); }, 0, row.chunks);
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+                if (own[g] > -INFINITY)
+                    add64(&sh.bin[min(int(fminf((top - own[g]) * scale, float(kSearch))), kSearch - 1)], 1);
             __syncthreads();
             uint64_t before, target, all = 0;
             const int last = find_bin(sh, sh.bin[2 * t], sh.bin[2 * t + 1],
@@ -992,8 +1007,9 @@ __device__ __forceinline__ void sample_row(Shared &sh, const SampleArgs &args, i
                 // the roundings of a bin are far below 2^-20 of its distance and 2^-22 of top
                 const float edge = top - float(last + 1) / scale * 1.000001f - fabsf(top) * 2.4e-7f;
                 const float from = fmaxf(edge, floor);
-                const uint32_t n = by_thread ? row.collect_from(sh, from, own)
-                                             : row.template collect<true>(sh, from, INFINITY);
+                // a wave takes about as long for one thread's place as for 64 threads' chunk
+                const uint32_t n = set.top_k <= 128 ? row.collect_from(sh, from, mine)
+                                                    : row.template collect<false>(sh, from, INFINITY);
                 if (n <= kList) return draw_from_list(sh, out, r, n, weight, set, least, uint32_t(row.v), value);
             }
         }
@@ -1035,15 +1051,15 @@ __device__ __forceinline__ void sample_row(Shared &sh, const SampleArgs &args, i
     }
     if (t < kSegs) sh.seg[t] = 0;
     __syncthreads();
-#pragma unroll
-    for (int s = 0; s < kSegs; ++s) {
-        uint64_t sum = 0;
-        if (2 * t < min(b, kMass - 1)) sum = weight.whole(sh.bin[s * kStride + kMass - 1 - 2 * t], 2 * t);
-        if (2 * t + 1 < min(b, kMass - 1)) sum += weight.whole(sh.bin[s * kStride + kMass - 2 - 2 * t], 2 * t + 1);
-        if (__any(sum != 0)) {
-            sum = wave_add(sum);
-            if ((t & 63) == 0) add64(&sh.seg[s], sum);
-        }
+    {
+        // 128 threads an eighth, a bin in 128 each, summed in 64-bit floating point in a fixed order
+        constexpr int kEach = kThreads / kSegs;
+        const int s = t / kEach;
+        double sum = 0.0;
+        for (int i = t % kEach; i < min(b, kMass - 1); i += kEach)
+            sum = fma(double(sh.bin[s * kStride + kMass - 1 - i]), weight.zero[-i] * weight.per_unit, sum);
+        const uint64_t all = wave_add(uint64_t(__builtin_rint(sum)));
+        if ((t & 63) == 0) add64(&sh.seg[s], all);
     }
     if (b < kMass) {
         if (t < 128) {
@@ -1053,9 +1069,7 @@ __device__ __forceinline__ void sample_row(Shared &sh, const SampleArgs &args, i
         }
         __syncthreads();
         const float lo = sh.edge[0], hi = sh.edge[1];
-        const uint32_t n = cut_k ? kList + 1
-                           : in_bin <= 256 ? row.template collect<true>(sh, lo, hi)
-                                           : row.template collect<false>(sh, lo, hi);
+        const uint32_t n = cut_k || in_bin > 2 * kList ? kList + 1 : row.template collect<true>(sh, lo, hi);
         if (n > kList) {
             if (by_p)
                 cut.from_key(border_in_row<T>(sh, row, true, weight, lo, hi, cut, target - before));
