@@ -320,12 +320,13 @@ rt_status rt_matmul_int8(const int8_t *a, int64_t lda, const float *a_scale, con
  * rt_quantize_rows_int8 of the activations x (m rows of k, fp32, bf16 or fp16)
  * followed by rt_matmul_int8 with the int8 rows w (n rows of k): the same
  * numbers as the two calls.  `workspace` is device memory of at least
- * rt_linear_int8_workspace(m, k) bytes, 16-byte aligned, that the call uses for
+ * rt_linear_int8_workspace(m, n, k) bytes, 16-byte aligned, that the call uses for
  * the quantised activations until its work on `stream` is done: calls that may
  * run at the same time (other streams, other graphs) need one each.
- * rt_linear_int8_workspace returns 0 for m = 0, -1 for sizes the call refuses.
+ * rt_linear_int8_workspace returns 0 where none is needed (m = 0, and a few short
+ * activations, which one kernel takes whole), -1 for sizes the call refuses.
  */
-int64_t rt_linear_int8_workspace(int64_t m, int32_t k);
+int64_t rt_linear_int8_workspace(int64_t m, int64_t n, int32_t k);
 rt_status rt_linear_int8(const void *x, int32_t dtype, int64_t ldx, const int8_t *w, int64_t ldw,
                          const float *w_scale, const float *bias, void *out, int32_t out_dtype, int64_t ldo,
                          int64_t m, int64_t n, int32_t k, void *workspace, int64_t workspace_bytes, void *stream);

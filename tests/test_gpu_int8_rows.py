@@ -112,7 +112,8 @@ def test_quantize_strided_input_and_given_outputs():
 
 
 # Sizes that end inside every tile of every kernel, one activation to many.
-SIZES = [(1, 1, 1), (1, 5, 3), (1, 64, 64), (2, 33, 127), (7, 1000, 128), (16, 17, 129), (17, 130, 320),
+SIZES = [(40, 40000, 128), (70, 33000, 130), (300, 17000, 1027), (520, 9000, 256), (200, 5000, 384), (33, 8000, 64),
+         (1, 1, 1), (1, 5, 3), (1, 64, 64), (2, 33, 127), (7, 1000, 128), (16, 17, 129), (17, 130, 320),
          (33, 65, 4096), (64, 256, 768), (65, 129, 200), (100, 1, 256), (128, 128, 128), (129, 300, 257),
          (200, 511, 1000), (300, 700, 64), (255, 257, 384), (513, 513, 640)]
 
@@ -159,8 +160,9 @@ def test_matmul_largest_sums(m, k):
 
 
 @pytest.mark.parametrize("dtype", list(TYPES))
-@pytest.mark.parametrize("m,n,k", [(1, 77, 100), (1, 1024, 1024), (3, 500, 768), (4, 96, 4096), (5, 96, 1000),
-                                   (31, 200, 777), (80, 300, 640), (270, 530, 129)])
+@pytest.mark.parametrize("m,n,k", [(1, 77, 100), (1, 1024, 1024), (1, 8, 8192), (1, 300, 8193), (1, 8193, 64),
+                                   (3, 500, 768), (4, 33, 2048), (4, 96, 4096), (5, 96, 1000), (31, 200, 777),
+                                   (80, 300, 640), (270, 530, 129)])
 def test_linear_is_quantize_then_product(dtype, m, n, k):
     g = torch.Generator().manual_seed(m + n + k)
     x = torch.randn(m, k, generator=g).to(TYPES[dtype]).cuda()
@@ -171,7 +173,7 @@ def test_linear_is_quantize_then_product(dtype, m, n, k):
     check(y, q, s.astype(np.float32), host(w), host(sw))
     two = matmul_int8(*quantize_rows_int8(x), w, sw, out_dtype=x.dtype)
     assert torch.equal(y, two)  # the same numbers as the two calls
-    ws = torch.empty(max(1, linear_int8_workspace(m, k)), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(max(1, linear_int8_workspace(m, n, k)), dtype=torch.uint8, device="cuda")
     assert torch.equal(y, linear_int8(x, w, sw, workspace=ws, out=torch.empty_like(y)))
 
 

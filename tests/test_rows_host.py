@@ -52,10 +52,12 @@ def test_check_matmul(lib):
 
 def test_linear_workspace(lib):
     f = lib.rt_linear_int8_workspace
-    assert f(-1, 64) == -1 and f(4, 0) == -1 and f(4, 65537) == -1 and f(2 ** 31, 64) == -1
-    assert f(0, 64) == 0
-    for m, k in ((1, 1), (100, 777), (2 ** 31 - 1, 65536)):
-        assert f(m, k) >= 0
+    for bad in ((-1, 8, 64), (4, 8, 0), (4, 8, 65537), (2 ** 31, 8, 64), (4, 0, 64), (4, 2 ** 31, 64)):
+        assert f(*bad) == -1, bad
+    assert f(0, 8, 64) == 0
+    for m, n, k in ((1, 1, 1), (100, 5, 777), (2 ** 31 - 1, 2 ** 31 - 1, 65536)):
+        need = f(m, n, k)
+        assert need == 0 or need >= m * k + 4 * m  # all codes and scales, or none at all
 
 
 def test_linear_refuses_before_anything_runs(lib):
@@ -98,7 +100,7 @@ def test_binding_refuses_host_tensors():
         with pytest.raises(TypeError):
             call()
     with pytest.raises(rt.ResidentTopKError):
-        rt.linear_int8_workspace(-1, 4)
+        rt.linear_int8_workspace(-1, 4, 4)
     with pytest.raises(rt.ResidentTopKError):
         rt.sample_rows_workspace(1, 0)
 

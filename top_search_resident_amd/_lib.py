@@ -99,7 +99,7 @@ def load():
         "rt_quantize_rows_int8": ([vp, i32, i64, i32, i64, vp, i64, vp, vp], ctypes.c_int),
         "rt_matmul_int8": ([vp, i64, vp, vp, i64, vp, vp, vp, i32, i64, i64, i64, i32, vp], ctypes.c_int),
         "rt_linear_int8": ([vp, i32, i64, vp, i64, vp, vp, vp, i32, i64, i64, i64, i32, vp, i64, vp], ctypes.c_int),
-        "rt_linear_int8_workspace": ([i64, i32], i64),
+        "rt_linear_int8_workspace": ([i64, i64, i32], i64),
         "rt_sample_rows": ([vp, i32, i64, i64, i64, vp, ctypes.POINTER(SampleSettings), vp, vp, vp, i64, vp],
                            ctypes.c_int),
         "rt_sample_rows_workspace": ([i64, i64], i64),

@@ -23,6 +23,7 @@
 
 #include "../../include/resident_topk.h"
 #include "float_types.hpp"
+#include "large_lds.hpp"
 #include "lds_dma.hpp"
 #include "limits.hpp"
 
@@ -47,9 +48,35 @@ __device__ __forceinline__ int nearest_quotient(float x, float s, float inv) {
     return static_cast<int>(n);
 }
 
-// One workgroup per row: the largest magnitude, then the codes.  The magnitude
-// is compared as the bits of |x|, which also order infinities and NaN above
-// every finite value.  Bound by the read of x; the second pass takes up to
+// A row's scale from the bits of its largest magnitude, which order infinities
+// and NaN above every finite value; *inv is 0 where all codes are.
+__device__ __forceinline__ float row_scale(uint32_t top, float *inv) {
+    float s = __uint_as_float(top) / 127.0f;
+    const bool finite = top < 0x7f800000u;
+    if (s < 1.17549435e-38f) s = 0.0f;
+    *inv = finite && s > 0.0f ? 1.0f / s : 0.0f;
+    return finite ? s : __builtin_nanf("");
+}
+template <typename T>
+__device__ __forceinline__ uint32_t magnitude(u32x4 v, uint32_t top) {
+#pragma unroll
+    for (int e = 0; e < int(16 / sizeof(T)); ++e) top = max(top, __float_as_uint(element<T>(v, e)) & 0x7fffffffu);
+    return top;
+}
+// The codes of 16 bytes of T, 4 to a word.
+template <typename T>
+__device__ __forceinline__ void codes16(u32x4 v, float s, float inv, uint32_t (&w)[4 / sizeof(T)]) {
+#pragma unroll
+    for (int g = 0; g < int(4 / sizeof(T)); ++g) {
+        w[g] = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            w[g] |= (uint32_t(nearest_quotient(element<T>(v, g * 4 + e), s, inv)) & 0xffu) << (8 * e);
+        if (inv == 0.0f) w[g] = 0;
+    }
+}
+
+// One workgroup per row: the largest magnitude, then the codes.  Bound by the read of x; the second pass takes up to
 // kQuantKeep chunks per thread from registers and the rest from L2.
 template <typename T>
 __global__ __launch_bounds__(kQuantThreads) void quantize_kernel(const T *x, int64_t ldx, int64_t m, int k,
@@ -68,16 +95,11 @@ __global__ __launch_bounds__(kQuantThreads) void quantize_kernel(const T *x, int
             const int i = c * kQuantThreads + t;
             if (i < whole) {
                 keep[c] = load16(xr + int64_t(i) * E);
-#pragma unroll
-                for (int e = 0; e < E; ++e)
-                    top = max(top, __float_as_uint(element<T>(keep[c], e)) & 0x7fffffffu);
+                top = magnitude<T>(keep[c], top);
             }
         }
-        for (int i = kQuantKeep * kQuantThreads + t; i < whole; i += kQuantThreads) {
-            const u32x4 v = load16(xr + int64_t(i) * E);
-#pragma unroll
-            for (int e = 0; e < E; ++e) top = max(top, __float_as_uint(element<T>(v, e)) & 0x7fffffffu);
-        }
+        for (int i = kQuantKeep * kQuantThreads + t; i < whole; i += kQuantThreads)
+            top = magnitude<T>(load16(xr + int64_t(i) * E), top);
         if (t < k - whole * E)
             top = max(top, __float_as_uint(static_cast<float>(xr[whole * E + t])) & 0x7fffffffu);
 #pragma unroll
@@ -88,23 +110,12 @@ __global__ __launch_bounds__(kQuantThreads) void quantize_kernel(const T *x, int
 #pragma unroll
         for (int w = 0; w < kQuantThreads / 64; ++w) top = max(top, wave_max[w]);
 
-        float s = __uint_as_float(top) / 127.0f;
-        const bool finite = top < 0x7f800000u;
-        if (s < 1.17549435e-38f) s = 0.0f;
-        const bool live = finite && s > 0.0f;
-        if (t == 0) scale[row] = finite ? s : __builtin_nanf("");
-        const float inv = live ? 1.0f / s : 0.0f;
-
+        float inv;
+        const float s = row_scale(top, &inv);
+        if (t == 0) scale[row] = s;
         auto codes = [&](int i, u32x4 v) {
-            uint32_t w[E / 4];
-#pragma unroll
-            for (int g = 0; g < E / 4; ++g) {
-                w[g] = 0;
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    w[g] |= (uint32_t(nearest_quotient(element<T>(v, g * 4 + e), s, inv)) & 0xffu) << (8 * e);
-                if (!live) w[g] = 0;
-            }
+            uint32_t w[4 / sizeof(T)];
+            codes16<T>(v, s, inv, w);
             __builtin_memcpy(qr + int64_t(i) * E, w, E);
         };
 #pragma unroll
@@ -114,7 +125,7 @@ __global__ __launch_bounds__(kQuantThreads) void quantize_kernel(const T *x, int
             codes(i, load16(xr + int64_t(i) * E));
         if (t < k - whole * E) {
             const int i = whole * E + t;
-            qr[i] = live ? int8_t(nearest_quotient(static_cast<float>(xr[i]), s, inv)) : int8_t(0);
+            qr[i] = inv != 0.0f ? int8_t(nearest_quotient(static_cast<float>(xr[i]), s, inv)) : int8_t(0);
         }
         for (int i = k + t; i < kpad; i += kQuantThreads) qr[i] = 0;
     }
@@ -130,48 +141,69 @@ struct Product {
     int64_t ldo;
     int64_t m, n;
     int k;
-    bool vec_out;  // four neighbouring outputs may be stored at once
+    bool vec_out;  // 16 bytes of neighbouring outputs may be stored at once
+
+    __device__ __forceinline__ const int8_t *a_end() const { return a + (m - 1) * lda + k; }
+    __device__ __forceinline__ const int8_t *b_end() const { return b + (n - 1) * ldb + k; }
 };
 
 __device__ __forceinline__ i32x4 mfma16(i32x4 a, i32x4 b, i32x4 c) {
     return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
 }
 
-// Up to 16 bytes at p, of which `valid` (possibly <= 0) exist; zeros elsewhere.
-__device__ __forceinline__ i32x4 load_part(const int8_t *p, int valid) {
-    if (valid >= 16) return __builtin_bit_cast(i32x4, load16(p));
+// 16 bytes at p, of which the first `valid` (any number) count and the rest read
+// as zeros.  They are read whole where they end before `end`, the end of the
+// matrix's last row, and byte by byte behind that.
+__device__ __forceinline__ i32x4 load_part(const int8_t *p, int valid, const int8_t *end) {
     i32x4 v = {0, 0, 0, 0};
+    if (valid <= 0) return v;
+    if (p + 16 <= end) {
+        v = __builtin_bit_cast(i32x4, load16(p));
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            const int n = min(max(valid - 4 * d, 0), 4);
+            v[d] &= int(uint32_t((uint64_t(1) << (8 * n)) - 1));
+        }
+        return v;
+    }
 #pragma unroll
     for (int i = 0; i < 16; ++i)
         if (i < valid) v[i >> 2] |= int(uint32_t(uint8_t(p[i])) << (8 * (i & 3)));
     return v;
 }
 
-// Scales, bias and rounding of the sums of output row i, columns j .. j + 3
-// (i < m; columns from n on are dropped).
-template <typename O>
-__device__ __forceinline__ void store4(const Product &p, int64_t i, int64_t j, i32x4 sum) {
-    const float sa = p.a_scale[i];
-    float y[4];
+// Scales, bias and rounding of the sums of output row i, columns j .. j + N - 1
+// (i < m; columns from n on are dropped).  NT: past the caches' keeping, for
+// outputs written in whole 64-byte pieces.
+template <int N, bool NT, typename O>
+__device__ __forceinline__ void store_row(const Product &p, int64_t i, int64_t j, const int32_t (&sum)[N], float sa) {
+    typedef O Piece __attribute__((ext_vector_type(N)));
+    Piece v;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        y[e] = 0.0f;
+    for (int e = 0; e < N; ++e) {
+        float y = 0.0f;
         if (j + e < p.n) {
-            y[e] = static_cast<float>(sum[e]) * sa * p.b_scale[j + e];
-            if (p.bias) y[e] += p.bias[j + e];
+            y = static_cast<float>(sum[e]) * sa * p.b_scale[j + e];
+            if (p.bias) y += p.bias[j + e];
         }
+        v[e] = static_cast<O>(y);
     }
     O *o = static_cast<O *>(p.out) + i * p.ldo + j;
-    if (p.vec_out && j + 4 <= p.n) {
-        O v[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = static_cast<O>(y[e]);
-        __builtin_memcpy(__builtin_assume_aligned(o, 4 * sizeof(O)), v, sizeof(v));
+    if (p.vec_out && j + N <= p.n) {
+        if (NT)
+            __builtin_nontemporal_store(v, reinterpret_cast<Piece *>(o));
+        else
+            *reinterpret_cast<Piece *>(o) = v;
     } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (j + e < p.n) o[e] = static_cast<O>(y[e]);
+        for (int e = 0; e < N; ++e)
+            if (j + e < p.n) o[e] = v[e];
     }
+}
+template <typename O>
+__device__ __forceinline__ void store4(const Product &p, int64_t i, int64_t j, i32x4 sum) {
+    const int32_t s[4] = {sum[0], sum[1], sum[2], sum[3]};
+    store_row<4, false, O>(p, i, j, s, p.a_scale[i]);
 }
 
 // direct: MF * 16 activations by NF * 16 rows b per workgroup of KW waves; wave w
@@ -217,10 +249,10 @@ __global__ __launch_bounds__(64 * KW) void direct_kernel(Product p, int64_t tile
                 const int valid = p.k - k0 - g * 16;
                 i32x4 av[MF];
 #pragma unroll
-                for (int f = 0; f < MF; ++f) av[f] = load_part(ap[f] + k0, valid);
+                for (int f = 0; f < MF; ++f) av[f] = load_part(ap[f] + k0, valid, p.a_end());
 #pragma unroll
                 for (int f = 0; f < NF; ++f) {
-                    const i32x4 bv = load_part(bp[f] + k0, valid);
+                    const i32x4 bv = load_part(bp[f] + k0, valid, p.b_end());
 #pragma unroll
                     for (int h = 0; h < MF; ++h) acc[f][h] = mfma16(bv, av[h], acc[f][h]);
                 }
@@ -242,6 +274,93 @@ __global__ __launch_bounds__(64 * KW) void direct_kernel(Product p, int64_t tile
     }
 }
 
+// few: rt_linear_int8 of a few short activations against not too many rows in
+// one launch (limits.hpp: int8_few).  Each workgroup of KW waves quantises all
+// of x into LDS while the first of its 16 rows b are on their way, then goes on
+// as the direct kernel.  Two launches cost a gap and a round trip of the codes
+// through memory: 1 x 4096 x 4096 6.4 us against 8.9, 1 x 1024 x 1024 4.3
+// against 5.9; but every workgroup repeats the quantising (4 x 4096 x 4096: 10.9
+// against 9.3), hence the limit.
+template <int KW, typename T, typename O>
+__global__ __launch_bounds__(64 * KW) void few_kernel(const T *x, int64_t ldx, Product p) {
+    constexpr int E = 16 / sizeof(T), kThreads = 64 * KW;
+    extern __shared__ __align__(16) int8_t codes[];  // m rows of kpad bytes
+    __shared__ i32x4 part[KW][64];
+    __shared__ uint32_t top[kInt8FewRows];
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    const int r16 = lane & 15, g = lane >> 4;
+    const int m = int(p.m), kpad = (p.k + 127) / 128 * 128, whole = p.k / E, blocks = p.k / 128;
+    const int8_t *bp = p.b + min(blockIdx.x * int64_t(16) + r16, p.n - 1) * p.ldb + g * 16;
+
+    i32x4 b0 = {0, 0, 0, 0}, b1 = {0, 0, 0, 0};
+    if (wave < blocks) {
+        b0 = __builtin_bit_cast(i32x4, load16(bp + wave * 128));
+        b1 = __builtin_bit_cast(i32x4, load16(bp + wave * 128 + 64));
+    }
+    if (t < kInt8FewRows) top[t] = 0;
+    __syncthreads();
+    for (int i = 0; i < m; ++i) {
+        const T *xr = x + i * ldx;
+        uint32_t own = 0;
+        for (int c = t; c < whole; c += kThreads) own = magnitude<T>(load16(xr + c * E), own);
+        if (t < p.k - whole * E) own = max(own, __float_as_uint(static_cast<float>(xr[whole * E + t])) & 0x7fffffffu);
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) own = max(own, uint32_t(__shfl_xor(int(own), o)));
+        if (lane == 0) atomicMax(&top[i], own);
+    }
+    __syncthreads();
+    for (int i = 0; i < m; ++i) {
+        const T *xr = x + i * ldx;
+        float inv;
+        const float s = row_scale(top[i], &inv);
+        for (int c = t; c < whole; c += kThreads) {
+            uint32_t w[4 / sizeof(T)];
+            codes16<T>(load16(xr + c * E), s, inv, w);
+            __builtin_memcpy(codes + i * kpad + c * E, w, E);
+        }
+        for (int c = whole * E + t; c < kpad; c += kThreads)
+            codes[i * kpad + c] =
+                c < p.k && inv != 0.0f ? int8_t(nearest_quotient(static_cast<float>(xr[c]), s, inv)) : int8_t(0);
+    }
+    __syncthreads();
+
+    const int8_t *ap = codes + min(r16, m - 1) * kpad + g * 16;
+    i32x4 acc = {0, 0, 0, 0};
+    for (int blk = wave; blk < blocks; blk += KW) {
+        if (blk != wave) {
+            b0 = __builtin_bit_cast(i32x4, load16(bp + blk * 128));
+            b1 = __builtin_bit_cast(i32x4, load16(bp + blk * 128 + 64));
+        }
+        acc = mfma16(b0, *reinterpret_cast<const i32x4 *>(ap + blk * 128), acc);
+        acc = mfma16(b1, *reinterpret_cast<const i32x4 *>(ap + blk * 128 + 64), acc);
+    }
+    if (wave == blocks % KW)  // the values after the last whole block; the codes behind them are 0
+        for (int k0 = blocks * 128; k0 < p.k; k0 += 64)
+            acc = mfma16(load_part(bp + k0, p.k - k0 - g * 16, p.b_end()),
+                         *reinterpret_cast<const i32x4 *>(ap + k0), acc);
+    part[wave][lane] = acc;
+    __syncthreads();
+    if (wave == 0) {
+        i32x4 sum = part[0][lane];
+#pragma unroll
+        for (int w = 1; w < KW; ++w) sum += part[w][lane];
+        const int64_t j = blockIdx.x * int64_t(16) + g * 4;
+        float inv;
+        if (r16 < m && j < p.n) {
+            const int32_t s4[4] = {sum[0], sum[1], sum[2], sum[3]};
+            store_row<4, false, O>(p, r16, j, s4, row_scale(top[r16], &inv));
+        }
+    }
+}
+
+template <typename T, typename O>
+hipError_t launch_few(const void *x, int64_t ldx, const Product &p, hipStream_t s) {
+    const int64_t tiles = (p.n + 15) / 16;
+    few_kernel<8, T, O><<<unsigned(tiles), 64 * 8, size_t(p.m) * size_t(int8_padded(p.k)), s>>>(
+        static_cast<const T *>(x), ldx, p);
+    return hipGetLastError();
+}
+
 // 16 bytes per lane from base + voff to LDS lds + 16 lane (kept in the caches:
 // other workgroups read the same rows).
 #pragma clang diagnostic push
@@ -256,13 +375,36 @@ __device__ __forceinline__ void dma16(const void *base, int voff, uint32_t lds) 
 // loads to LDS are waited for by wait_vmcnt).
 __device__ __forceinline__ void barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
-// tile: BM activations by BN rows b per workgroup of WM x WN waves.
-template <int BM, int BN, int WM, int WN, typename O>
+// The place of 16-byte unit u of a row among its 128 bytes is u ^ unit_swap(row).
+// ds_read_b128 serves lanes 0-3, 12-15 and 20-27 together, then 4-11, 16-19 and
+// 28-31, and so on: with r & 7 for rows read in order, and with the other for
+// the rows a two-byte output reads (row_of), each such 16 lanes hit all 64 banks
+// once (4.1 cycles a read; 8.0 with the bound kernels' dma_swizzle).
+template <bool PAIRS>
+__device__ __forceinline__ int unit_swap(int r) {
+    return PAIRS ? ((r >> 1) & 1) | (((r >> 3) & 3) << 1) : r & 7;
+}
+// Row, within a wave's rows b, of operand row r16 of fragment f.  A lane's four results
+// are operand rows 4 g .. 4 g + 3; two-byte outputs take the rows such that
+// fragments 2 q and 2 q + 1 give a lane 8 neighbouring columns: 16 bytes a
+// lane, and 64 contiguous bytes of a row in one store, for every output type.
+template <bool PAIRS>
+__device__ __forceinline__ int row_of(int f, int r16) {
+    return PAIRS ? (f >> 1) * 32 + (r16 >> 2) * 8 + (f & 1) * 4 + (r16 & 3) : f * 16 + r16;
+}
+
+// tile: BM activations by BN rows b per workgroup of WM x WN waves, STAGES
+// 128-byte steps of both in LDS.  Measured on 8192^3 (bf16 out): 256 x 256 with
+// 16 waves 2.5 PFLOP/s, with 8 waves 2.37 (a wave's LDS reads wait, the more
+// waves the better covered), 128 x 128 1.9.
+template <int BM, int BN, int WM, int WN, int STAGES, typename O>
 __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(Product p, int tiles_m, int tiles_n) {
     constexpr int NW = WM * WN, TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
     constexpr int LA = BM / 8 / NW, LB = BN / 8 / NW;  // LDS loads per wave and step
+    constexpr bool PAIRS = sizeof(O) == 2;
     static_assert(LA * 8 * NW == BM && LB * 8 * NW == BN, "whole loads per wave");
-    extern __shared__ __align__(1024) int8_t lds[];  // two buffers of (BM + BN) rows of 128 bytes
+    static_assert(!PAIRS || FN % 2 == 0, "pairs of fragments");
+    extern __shared__ __align__(1024) int8_t lds[];  // STAGES buffers of (BM + BN) rows of 128 bytes
     constexpr int kBuf = (BM + BN) * 128;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -270,15 +412,16 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(Product p, int tiles
     const int r16 = lane & 15, g = lane >> 4;
 
     // Neighbouring workgroup numbers go to different XCDs: give each XCD a
-    // contiguous run of tiles, and walk the tiles in groups of 8 tile rows so
-    // that the run shares its activations and rows in the XCD's L2.
+    // contiguous run of tiles, and walk the tiles in groups of 2048 activations
+    // so that the run shares its activations and rows in the XCD's L2.
     const uint32_t total = uint32_t(tiles_m) * uint32_t(tiles_n);  // < 2^31
     uint32_t id = blockIdx.x;
     const uint32_t per = total / 8;
     if (id < per * 8) id = (id % 8) * per + id / 8;
-    const uint32_t group = 8 * uint32_t(tiles_n);
-    const uint32_t first = id / group * 8;
-    const uint32_t rows = min(uint32_t(tiles_m) - first, 8u);
+    constexpr uint32_t kGroup = 2048 / BM;
+    const uint32_t group = kGroup * uint32_t(tiles_n);
+    const uint32_t first = id / group * kGroup;
+    const uint32_t rows = min(uint32_t(tiles_m) - first, kGroup);
     const int64_t tm = __builtin_amdgcn_readfirstlane(first + id % group % rows);
     const int64_t tn = __builtin_amdgcn_readfirstlane(id % group / rows);
     const int64_t i0 = tm * BM, j0 = tn * BN;
@@ -288,12 +431,12 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(Product p, int tiles
 #pragma unroll
     for (int i = 0; i < LA; ++i) {
         const int r = (i * NW + wave) * 8 + (lane >> 3);
-        av[i] = int(min(int64_t(r), p.m - 1 - i0) * p.lda) + (((lane & 7) ^ dma_swizzle(r)) * 16);
+        av[i] = int(min(int64_t(r), p.m - 1 - i0) * p.lda) + (((lane & 7) ^ unit_swap<false>(r)) * 16);
     }
 #pragma unroll
     for (int i = 0; i < LB; ++i) {
         const int r = (i * NW + wave) * 8 + (lane >> 3);
-        bv[i] = int(min(int64_t(r), p.n - 1 - j0) * p.ldb) + (((lane & 7) ^ dma_swizzle(r)) * 16);
+        bv[i] = int(min(int64_t(r), p.n - 1 - j0) * p.ldb) + (((lane & 7) ^ unit_swap<PAIRS>(r)) * 16);
     }
     const uint32_t lds0 = lds_addr(lds);
     auto stage = [&](int step, int buf) {
@@ -311,35 +454,38 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(Product p, int tiles
         for (int h = 0; h < FM; ++h) acc[f][h] = i32x4{0, 0, 0, 0};
 
     const int steps = p.k / 128;
-    if (steps > 0) stage(0, 0);
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s)
+        if (s < steps) stage(s, s);
+    int buf = 0;
     for (int step = 0; step < steps; ++step) {
-        if (step + 1 < steps) {
-            stage(step + 1, (step + 1) & 1);
-            wait_vmcnt<LA + LB>();
-        } else {
+        // this step's loads are the oldest of those in flight
+        if (step + STAGES - 2 < steps)
+            wait_vmcnt<(STAGES - 2) * (LA + LB)>();
+        else
             wait_vmcnt<0>();
-        }
-        barrier();  // every wave's loads of this step have landed
-        const int8_t *la = lds + (step & 1) * kBuf, *lb = la + BM * 128;
+        barrier();  // every wave's loads of this step have landed, its reads of the step before are done
+        if (step + STAGES - 1 < steps) stage(step + STAGES - 1, buf == 0 ? STAGES - 1 : buf - 1);
+        const int8_t *la = lds + buf * kBuf, *lb = la + BM * 128;
+        if (++buf == STAGES) buf = 0;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             i32x4 fa[FM], fb[FN];
 #pragma unroll
             for (int h = 0; h < FM; ++h) {
                 const int r = wm * TM + h * 16 + r16;
-                fa[h] = *reinterpret_cast<const i32x4 *>(la + r * 128 + (((s * 4 + g) ^ dma_swizzle(r)) * 16));
+                fa[h] = *reinterpret_cast<const i32x4 *>(la + r * 128 + (((s * 4 + g) ^ unit_swap<false>(r)) * 16));
             }
 #pragma unroll
             for (int f = 0; f < FN; ++f) {
-                const int r = wn * TN + f * 16 + r16;
-                fb[f] = *reinterpret_cast<const i32x4 *>(lb + r * 128 + (((s * 4 + g) ^ dma_swizzle(r)) * 16));
+                const int r = wn * TN + row_of<PAIRS>(f, r16);
+                fb[f] = *reinterpret_cast<const i32x4 *>(lb + r * 128 + (((s * 4 + g) ^ unit_swap<PAIRS>(r)) * 16));
             }
 #pragma unroll
             for (int f = 0; f < FN; ++f)
 #pragma unroll
                 for (int h = 0; h < FM; ++h) acc[f][h] = mfma16(fb[f], fa[h], acc[f][h]);
         }
-        barrier();  // this buffer may be overwritten
     }
     // the values after the last whole step, straight from global memory
     for (int k0 = steps * 128; k0 < p.k; k0 += 64) {
@@ -347,23 +493,30 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(Product p, int tiles
         i32x4 fa[FM];
 #pragma unroll
         for (int h = 0; h < FM; ++h)
-            fa[h] = load_part(p.a + min(i0 + wm * TM + h * 16 + r16, p.m - 1) * p.lda + k0 + g * 16, valid);
+            fa[h] = load_part(p.a + min(i0 + wm * TM + h * 16 + r16, p.m - 1) * p.lda + k0 + g * 16, valid, p.a_end());
 #pragma unroll
         for (int f = 0; f < FN; ++f) {
             const i32x4 fb =
-                load_part(p.b + min(j0 + wn * TN + f * 16 + r16, p.n - 1) * p.ldb + k0 + g * 16, valid);
+                load_part(p.b + min(j0 + wn * TN + row_of<PAIRS>(f, r16), p.n - 1) * p.ldb + k0 + g * 16, valid,
+                          p.b_end());
 #pragma unroll
             for (int h = 0; h < FM; ++h) acc[f][h] = mfma16(fb, fa[h], acc[f][h]);
         }
     }
+    // 16 bytes a lane: 4 columns of fp32, 8 of a two-byte type
+    constexpr int kSide = PAIRS ? 2 : 1;
 #pragma unroll
     for (int h = 0; h < FM; ++h) {
         const int64_t i = i0 + wm * TM + h * 16 + r16;
         if (i >= p.m) continue;
+        const float sa = p.a_scale[i];
 #pragma unroll
-        for (int f = 0; f < FN; ++f) {
-            const int64_t j = j0 + wn * TN + f * 16 + g * 4;
-            if (j < p.n) store4<O>(p, i, j, acc[f][h]);
+        for (int f = 0; f < FN; f += kSide) {
+            const int64_t j = j0 + wn * TN + f * 16 + g * 4 * kSide;
+            int32_t sum[4 * kSide];
+#pragma unroll
+            for (int e = 0; e < 4 * kSide; ++e) sum[e] = acc[f + e / 4][h][e % 4];
+            if (j < p.n) store_row<4 * kSide, true, O>(p, i, j, sum, sa);
         }
     }
 }
@@ -377,14 +530,14 @@ hipError_t launch_direct(const Product &p, hipStream_t s) {
     return hipGetLastError();
 }
 
-template <int BM, int BN, int WM, int WN, typename O>
+template <int BM, int BN, int WM, int WN, int STAGES, typename O>
 hipError_t launch_tile(const Product &p, hipStream_t s) {
     const int64_t tiles_m = (p.m + BM - 1) / BM, tiles_n = (p.n + BN - 1) / BN;
-    constexpr int kLds = 2 * (BM + BN) * 128;
-    auto *kernel = tile_kernel<BM, BN, WM, WN, O>;
+    constexpr int kLds = STAGES * (BM + BN) * 128;
+    auto *kernel = tile_kernel<BM, BN, WM, WN, STAGES, O>;
     if (kLds > 64 * 1024) {
-        hipError_t err = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+        static std::atomic<uint64_t> told{0};
+        hipError_t err = allow_lds(reinterpret_cast<const void *>(kernel), kLds, told);
         if (err != hipSuccess) return err;
     }
     kernel<<<unsigned(tiles_m * tiles_n), 64 * WM * WN, kLds, s>>>(p, int(tiles_m), int(tiles_n));
@@ -397,17 +550,32 @@ bool aligned16(const void *ptr, int64_t ld) {
 
 template <typename O>
 hipError_t launch_product(Product p, hipStream_t s) {
-    p.vec_out = (reinterpret_cast<uintptr_t>(p.out) % (4 * sizeof(O))) == 0 && p.ldo % 4 == 0;
-    // a tile's row offsets are 32-bit: 255 ld + depth
-    // and a grid has fewer than 2^32 threads
-    const bool tiles = aligned16(p.a, p.lda) && aligned16(p.b, p.ldb) && p.lda <= (1 << 22) && p.ldb <= (1 << 22) &&
-                       ((p.m + 127) / 128) * ((p.n + 127) / 128) < (1 << 23);
-    if (p.m <= 16) return launch_direct<1, 1, 8, O>(p, s);
-    if (p.m <= 32) return launch_direct<2, 2, 8, O>(p, s);
-    if (p.m <= 64 || !tiles) return launch_direct<4, 2, 4, O>(p, s);
-    const int64_t big = (p.m + 255) / 256 * ((p.n + 255) / 256);
-    if (big >= 256) return launch_tile<256, 256, 2, 4, O>(p, s);
-    return launch_tile<128, 128, 2, 2, O>(p, s);
+    p.vec_out = reinterpret_cast<uintptr_t>(p.out) % 16 == 0 && p.ldo % (16 / sizeof(O)) == 0;
+    auto tiles = [&](int64_t bm, int64_t bn) { return ((p.m + bm - 1) / bm) * ((p.n + bn - 1) / bn); };
+    // a tile's row offsets are 32-bit: 255 ld + depth; and a grid has fewer than 2^32 threads
+    const bool in_tiles = aligned16(p.a, p.lda) && aligned16(p.b, p.ldb) && p.lda <= (1 << 22) && p.ldb <= (1 << 22) &&
+                          tiles(128, 128) < (1 << 22);
+    if (p.m <= 16 && (p.n <= 8192 || !in_tiles)) return launch_direct<1, 1, 8, O>(p, s);
+    if (!in_tiles) return launch_direct<4, 2, 4, O>(p, s);
+    // The largest tile, not much higher than m, that still gives each of the 256
+    // CUs one.  Measured (us, fp32 out, bf16 for the first two rows):
+    //   m x n x k             256x256  128x128  128x64  64x64  32x64  32x32  direct
+    //   4 x 8192 x 8192                                 19.0   17.4   16.6   14.0
+    //   32 x 16384 x 4096                               13.7   13.1   13.2   18.8
+    //   8192 x 8192 x 1024    119      121      129     291
+    //   1024 x 8192 x 4096    51.6     39.6     51.7    68.8
+    //   512 x 4096 x 2048              17.3     12.0    12.6   15.0   15.3   21.5
+    //   256 x 4096 x 4096              25.7     16.5    13.7   12.5   15.5   25.9
+    //   1024 x 1024 x 1024             12.4     8.6     7.3    6.6    6.8    10.1
+    //   77 x 1001 x 777                12.6     9.7     9.4    6.6    5.0    6.5
+    if (p.m > 128 && p.k >= 1024 && tiles(256, 256) >= 256) return launch_tile<256, 256, 4, 4, 2, O>(p, s);
+    if (p.m > 64 && tiles(128, 128) >= 256) return launch_tile<128, 128, 4, 4, 2, O>(p, s);
+    if (p.m > 64 && tiles(128, 64) >= 256) return launch_tile<128, 64, 4, 2, 3, O>(p, s);
+    if (p.m > 32 && tiles(64, 64) >= 512) return launch_tile<64, 64, 2, 2, 4, O>(p, s);
+    // 1 x 100000 x 768: 32 x 128 17.0, 32 x 64 18.3; 1 x 50000 x 1024: 9.8, 12.2
+    if (tiles(32, 128) >= 256) return launch_tile<32, 128, 1, 4, 4, O>(p, s);
+    if (tiles(32, 64) >= 256) return launch_tile<32, 64, 2, 2, 4, O>(p, s);
+    return launch_tile<32, 32, 2, 1, 4, O>(p, s);
 }
 
 hipError_t launch_quantize(const void *x, int32_t dtype, int64_t m, int32_t k, int64_t ldx, int8_t *q, int64_t ldq,
@@ -431,6 +599,24 @@ hipError_t launch_matmul(const Product &p, int32_t out_dtype, hipStream_t s) {
         case RT_DTYPE_FLOAT32: return launch_product<float>(p, s);
         case RT_DTYPE_BFLOAT16: return launch_product<bf16_t>(p, s);
         default: return launch_product<fp16_t>(p, s);
+    }
+}
+
+template <typename T>
+hipError_t launch_few_as(const void *x, int64_t ldx, const Product &p, int32_t out_dtype, hipStream_t s) {
+    switch (out_dtype) {
+        case RT_DTYPE_FLOAT32: return launch_few<T, float>(x, ldx, p, s);
+        case RT_DTYPE_BFLOAT16: return launch_few<T, bf16_t>(x, ldx, p, s);
+        default: return launch_few<T, fp16_t>(x, ldx, p, s);
+    }
+}
+
+hipError_t launch_few_rows(const void *x, int32_t dtype, int64_t ldx, Product p, int32_t out_dtype, hipStream_t s) {
+    p.vec_out = reinterpret_cast<uintptr_t>(p.out) % 16 == 0 && p.ldo % (out_dtype == RT_DTYPE_FLOAT32 ? 4 : 8) == 0;
+    switch (dtype) {
+        case RT_DTYPE_FLOAT32: return launch_few_as<float>(x, ldx, p, out_dtype, s);
+        case RT_DTYPE_BFLOAT16: return launch_few_as<bf16_t>(x, ldx, p, out_dtype, s);
+        default: return launch_few_as<fp16_t>(x, ldx, p, out_dtype, s);
     }
 }
 
@@ -464,18 +650,26 @@ rt_status rt_matmul_int8(const int8_t *a, int64_t lda, const float *a_scale, con
 rt_status rt_linear_int8(const void *x, int32_t dtype, int64_t ldx, const int8_t *w, int64_t ldw,
                          const float *w_scale, const float *bias, void *out, int32_t out_dtype, int64_t ldo,
                          int64_t m, int64_t n, int32_t k, void *workspace, int64_t workspace_bytes, void *stream) {
-    const int64_t need = rt_linear_int8_workspace(m, k);
+    const int64_t need = rt_linear_int8_workspace(m, n, k);
     if (need < 0) return RT_EINVAL;
-    if (m > 0 && (workspace == nullptr || workspace_bytes < need ||
-                  (reinterpret_cast<uintptr_t>(workspace) & 15u) != 0))
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need ||
+                     (reinterpret_cast<uintptr_t>(workspace) & 15u) != 0))
         return RT_EINVAL;
+    // with few rows the codes stay in LDS; the checks only look at their place
+    static const float none = 0.0f;
     const int64_t ldq = rt::int8_padded(k);
-    int8_t *q = static_cast<int8_t *>(workspace);
-    float *scale = m > 0 ? reinterpret_cast<float *>(q + m * ldq) : nullptr;
-    rt_status st = rt_check_quantize_rows_int8(x, dtype, m, k, ldx, q, ldq, scale);
+    int8_t *q = need > 0 ? static_cast<int8_t *>(workspace) : nullptr;
+    float *scale = need > 0 ? reinterpret_cast<float *>(q + m * ldq) : nullptr;
+    const void *place = need > 0 ? static_cast<const void *>(q) : &none;
+    rt_status st = rt_check_quantize_rows_int8(x, dtype, m, k, ldx, place, ldq, need > 0 ? scale : &none);
     if (st == RT_OK)
-        st = rt_check_matmul_int8(q, ldq, scale, w, ldw, w_scale, bias, out, out_dtype, ldo, m, n, k);
+        st = rt_check_matmul_int8(place, ldq, need > 0 ? scale : &none, w, ldw, w_scale, bias, out, out_dtype, ldo, m,
+                                  n, k);
     if (st != RT_OK || m == 0) return st;
+    if (need == 0) {
+        const rt::Product p{nullptr, w, 0, ldw, nullptr, w_scale, bias, out, ldo, m, n, k, false};
+        return rt::status_of(rt::launch_few_rows(x, dtype, ldx, p, out_dtype, static_cast<hipStream_t>(stream)));
+    }
     hipStream_t s = static_cast<hipStream_t>(stream);
     hipError_t err = rt::launch_quantize(x, dtype, m, k, ldx, q, ldq, int(ldq), scale, s);
     const rt::Product p{q, w, ldq, ldw, scale, w_scale, bias, out, ldo, m, n, k, false};

@@ -28,6 +28,7 @@
 
 #include "../../include/resident_topk.h"
 #include "float_types.hpp"
+#include "large_lds.hpp"
 #include "limits.hpp"
 
 namespace rt {
@@ -1108,8 +1109,8 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleArgs args, int64_t 
 
 template <typename T>
 hipError_t launch(const SampleArgs &a, hipStream_t s) {
-    hipError_t err = hipFuncSetAttribute(reinterpret_cast<const void *>(row_kernel<T>),
-                                         hipFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(Shared)));
+    static std::atomic<uint64_t> told{0};
+    hipError_t err = allow_lds(reinterpret_cast<const void *>(row_kernel<T>), int(sizeof(Shared)), told);
     // a workgroup per row: a loop over rows in the kernel would keep what the
     // passes have in common in registers across all of them
     constexpr int64_t kMost = 1 << 20;

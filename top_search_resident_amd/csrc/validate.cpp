@@ -104,8 +104,9 @@ rt_status rt_check_matmul_int8(const void *a, int64_t lda, const void *a_scale, 
     return RT_OK;
 }
 
-int64_t rt_linear_int8_workspace(int64_t m, int32_t k) {
-    if (m < 0 || m > kMaxN || k < 1 || k > rt::kMaxRowK) return -1;
+int64_t rt_linear_int8_workspace(int64_t m, int64_t n, int32_t k) {
+    if (m < 0 || m > kMaxN || n < 1 || n > kMaxN || k < 1 || k > rt::kMaxRowK) return -1;
+    if (m == 0 || rt::int8_few(m, n, k)) return 0;
     return m * rt::int8_padded(k) + (4 * m + 15) / 16 * 16;
 }
 

@@ -10,60 +10,61 @@ Matrices are 2-D with neighbouring elements in a row and any row stride.  The
 work is enqueued on `stream` (default: torch's current stream on the tensors'
 device); tensors made here belong to that stream.
 """
-import contextlib
 import ctypes
 
 from . import _lib
 from ._lib import SampleSettings
 
-_T = {}  # torch and what is looked up in it once
 
+class _Once:
+    """torch, the library and what is looked up in them once, at the first call."""
+    lib = None
 
-def _torch():
-    if not _T:
+    def load(self):
         import torch
-        _T.update(torch=torch, floats={torch.float32: _lib.RT_DTYPE_FLOAT32, torch.bfloat16: _lib.RT_DTYPE_BFLOAT16,
-                                       torch.float16: _lib.RT_DTYPE_FLOAT16},
-                  raw=getattr(torch._C, "_cuda_getCurrentRawStream", None))
-    return _T["torch"]
+        lib = _lib.load()
+        self.torch = torch
+        self.tensor = torch.Tensor
+        self.empty = torch.empty
+        self.fp32, self.int32, self.int8, self.uint8 = torch.float32, torch.int32, torch.int8, torch.uint8
+        self.floats = {torch.float32: _lib.RT_DTYPE_FLOAT32, torch.bfloat16: _lib.RT_DTYPE_BFLOAT16,
+                       torch.float16: _lib.RT_DTYPE_FLOAT16}
+        self.int8s = {torch.int8: None}
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # a tenth of current_stream()'s time
+        self.stream = raw or (lambda device: torch.cuda.current_stream(device).cuda_stream)
+        self.device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+        self.lib = lib
+        return self
 
 
-def _raise(status, what):
-    raise _lib.ResidentTopKError(status, what)
+_once = _Once()
 
 
-def _place(x, stream):
-    """(stream handle, context that makes x's device current and, with a stream of
-    the caller's, torch's allocations that stream's; None if nothing is to be entered)."""
-    torch = _torch()
+def _elsewhere(o, x, name, stream):
+    """None where x is on the current device and no stream is named; else the context to
+    call again in: x's device current and, with a stream, torch's allocations that stream's."""
+    if not isinstance(x, o.tensor):
+        raise TypeError(f"{name} must be a torch tensor")
     device = x.get_device()
     if device < 0:
-        raise TypeError("a CUDA tensor is needed")
+        raise TypeError(f"{name} must be a CUDA tensor")
     if stream is not None:
         if stream.device_index != device:
-            raise ValueError(f"the stream is on cuda:{stream.device_index}, the tensors on cuda:{device}")
-        return stream.cuda_stream, torch.cuda.stream(stream)
-    raw = _T["raw"]
-    handle = raw(device) if raw is not None else torch.cuda.current_stream(device).cuda_stream
-    if torch.cuda.current_device() != device:
-        return handle, torch.cuda.device(device)
-    return handle, None
+            raise ValueError(f"the stream is on cuda:{stream.device_index}, {name} on cuda:{device}")
+        return o.torch.cuda.stream(stream)
+    return None if o.device() == device else o.torch.cuda.device(device)
 
 
-def _matrix(t, name, dtypes, device):
+def _matrix(o, t, name, dtypes, device):
     """Rows, columns and row stride of a 2-D CUDA tensor whose rows are dense and do not overlap."""
-    torch = _T["torch"]
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, o.tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D, got {t.dim()}-D")
-    dev = t.get_device()
-    if dev != device:
-        if dev < 0:
-            raise TypeError(f"{name} must be a CUDA tensor")
-        raise ValueError(f"{name} is on {t.device}, the call on cuda:{device}")
+    if t.get_device() != device:
+        _wrong_device(t, name, device)
     rows, cols = t.shape
     ld, step = t.stride()
     if rows <= 1 or cols == 0:
@@ -73,17 +74,20 @@ def _matrix(t, name, dtypes, device):
     return rows, cols, ld
 
 
-def _vector(t, name, dtype, n, device):
-    torch = _T["torch"]
-    if not isinstance(t, torch.Tensor):
+def _wrong_device(t, name, device):
+    if t.get_device() < 0:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    raise ValueError(f"{name} is on {t.device}, the call on cuda:{device}")
+
+
+def _vector(o, t, name, dtype, n, device):
+    """Address of a contiguous CUDA tensor [n]."""
+    if not isinstance(t, o.tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    dev = t.get_device()
-    if dev != device:
-        if dev < 0:
-            raise TypeError(f"{name} must be a CUDA tensor")
-        raise ValueError(f"{name} is on {t.device}, the call on cuda:{device}")
+    if t.get_device() != device:
+        _wrong_device(t, name, device)
     if t.dim() != 1 or t.shape[0] != n:
         raise ValueError(f"{name} must have shape [{n}], got {list(t.shape)}")
     if n > 1 and t.stride(0) != 1:
@@ -91,11 +95,25 @@ def _vector(t, name, dtype, n, device):
     return t.data_ptr()
 
 
-def _out_matrix(out, m, n, device):
-    rows, cols, ld = _matrix(out, "out", _T["floats"], device)
+def _output(o, out, dtype, m, n, like, device):
+    """(out, its type's code, its row stride), made here where none is given."""
+    if out is None:
+        code = o.floats.get(dtype)
+        if code is None:
+            raise TypeError(f"out_dtype must be torch.float32, torch.bfloat16 or torch.float16, got {dtype}")
+        return o.empty((m, n), dtype=dtype, device=like.device), code, n
+    rows, cols, ld = _matrix(o, out, "out", o.floats, device)
     if rows != m or cols != n:
         raise ValueError(f"out must have shape [{m}, {n}], got {list(out.shape)}")
-    return ld
+    return out, o.floats[out.dtype], ld
+
+
+def _workspace(o, t, device):
+    if not isinstance(t, o.tensor) or t.dtype != o.uint8 or not t.is_contiguous():
+        raise TypeError("workspace must be a contiguous uint8 tensor")
+    if t.get_device() != device:
+        _wrong_device(t, "workspace", device)
+    return t.data_ptr(), t.numel()
 
 
 def quantize_rows_int8(x, out=None, out_scale=None, stream=None):
@@ -105,26 +123,29 @@ def quantize_rows_int8(x, out=None, out_scale=None, stream=None):
     have a row stride that is a multiple of 16 with zeros behind each row, the
     layout the products read fastest.  A row with an infinity or NaN gets scale
     NaN and zero codes."""
-    torch = _torch()
-    handle, context = _place(x, stream) if isinstance(x, torch.Tensor) else _matrix(x, "x", (), 0)
+    o = _once if _once.lib else _once.load()
+    context = _elsewhere(o, x, "x", stream)
+    if context is not None:
+        with context:
+            return quantize_rows_int8(x, out, out_scale)
     device = x.get_device()
-    m, k, ld = _matrix(x, "x", _T["floats"], device)
-    with context or contextlib.nullcontext():
-        if out is None:
-            pitch = (k + 15) // 16 * 16
-            out = torch.empty((m, pitch), dtype=torch.int8, device=x.device)
-            if pitch != k:
-                out[:, k:].zero_()
-                out = out[:, :k]
-        if out_scale is None:
-            out_scale = torch.empty(m, dtype=torch.float32, device=x.device)
-        rows, cols, ldq = _matrix(out, "out", (torch.int8,), device)
+    m, k, ld = _matrix(o, x, "x", o.floats, device)
+    if out is None:
+        ldq = (k + 15) // 16 * 16
+        out = o.empty((m, ldq), dtype=o.int8, device=x.device)
+        if ldq != k:
+            out[:, k:].zero_()
+            out = out[:, :k]
+    else:
+        rows, cols, ldq = _matrix(o, out, "out", o.int8s, device)
         if (rows, cols) != (m, k):
             raise ValueError(f"out must have shape [{m}, {k}], got {list(out.shape)}")
-        st = _lib.load().rt_quantize_rows_int8(x.data_ptr(), _T["floats"][x.dtype], m, k, ld, out.data_ptr(), ldq,
-                                               _vector(out_scale, "out_scale", torch.float32, m, device), handle)
+    if out_scale is None:
+        out_scale = o.empty(m, dtype=o.fp32, device=x.device)
+    st = o.lib.rt_quantize_rows_int8(x.data_ptr(), o.floats[x.dtype], m, k, ld, out.data_ptr(), ldq,
+                                     _vector(o, out_scale, "out_scale", o.fp32, m, device), o.stream(device))
     if st:
-        _raise(st, "quantize_rows_int8")
+        raise _lib.ResidentTopKError(st, "quantize_rows_int8")
     return out, out_scale
 
 
@@ -133,78 +154,67 @@ def matmul_int8(a, a_scale, b, b_scale, bias=None, out=None, out_dtype=None, str
     rows a [m, k] and b [n, k] with fp32 scales [m] and [n] and an fp32 bias [n].
     The sums are exact; the result is rounded once to out_dtype (default fp32), fp32, bf16
     or fp16.  Returns out [m, n]."""
-    torch = _torch()
-    handle, context = _place(a, stream) if isinstance(a, torch.Tensor) else _matrix(a, "a", (), 0)
-    device = a.get_device()
-    m, k, lda = _matrix(a, "a", (torch.int8,), device)
-    n, kb, ldb = _matrix(b, "b", (torch.int8,), device)
-    if kb != k:
-        raise ValueError(f"a has rows of {k}, b rows of {kb}")
-    sa = _vector(a_scale, "a_scale", torch.float32, m, device)
-    sb = _vector(b_scale, "b_scale", torch.float32, n, device)
-    pbias = None if bias is None else _vector(bias, "bias", torch.float32, n, device)
-    out, st = _product(context, out, out_dtype or torch.float32, m, n, a.device, device,
-                       lambda f, o, dt, ldo: f.rt_matmul_int8(a.data_ptr(), lda, sa, b.data_ptr(), ldb, sb, pbias, o,
-                                                              dt, ldo, m, n, k, handle))
-    if st:
-        _raise(st, "matmul_int8")
-    return out
-
-
-def _product(context, out, out_dtype, m, n, where, device, call):
+    o = _once if _once.lib else _once.load()
+    context = _elsewhere(o, a, "a", stream)
     if context is not None:
         with context:
-            return _product(None, out, out_dtype, m, n, where, device, call)
-    if out is None:
-        if out_dtype not in _T["floats"]:
-            raise TypeError(f"out_dtype must be torch.float32, torch.bfloat16 or torch.float16, got {out_dtype}")
-        out = _T["torch"].empty((m, n), dtype=out_dtype, device=where)
-        ldo = n
-    else:
-        ldo = _out_matrix(out, m, n, device)
-    return out, call(_lib.load(), out.data_ptr(), _T["floats"][out.dtype], ldo)
+            return matmul_int8(a, a_scale, b, b_scale, bias, out, out_dtype)
+    device = a.get_device()
+    m, k, lda = _matrix(o, a, "a", o.int8s, device)
+    n, kb, ldb = _matrix(o, b, "b", o.int8s, device)
+    if kb != k:
+        raise ValueError(f"a has rows of {k}, b rows of {kb}")
+    sa = _vector(o, a_scale, "a_scale", o.fp32, m, device)
+    sb = _vector(o, b_scale, "b_scale", o.fp32, n, device)
+    pbias = None if bias is None else _vector(o, bias, "bias", o.fp32, n, device)
+    out, code, ldo = _output(o, out, out_dtype or o.fp32, m, n, a, device)
+    st = o.lib.rt_matmul_int8(a.data_ptr(), lda, sa, b.data_ptr(), ldb, sb, pbias, out.data_ptr(), code, ldo, m, n, k,
+                              o.stream(device))
+    if st:
+        raise _lib.ResidentTopKError(st, "matmul_int8")
+    return out
 
 
 def linear_int8(x, w, w_scale, bias=None, out=None, out_dtype=None, workspace=None, stream=None):
     """matmul_int8(*quantize_rows_int8(x), w, w_scale, bias): activations x [m, k]
     (fp32, bf16 or fp16), quantised row by row, times int8 rows w [n, k].  Returns
     out [m, n] in out_dtype (default: x's type).  `workspace`: a uint8 CUDA tensor
-    of at least linear_int8_workspace(m, k) bytes, 16-byte aligned, for callers
+    of at least linear_int8_workspace(m, n, k) bytes, 16-byte aligned, for callers
     that keep one (one for each call that may run at the same time); by default
     one is taken from torch's allocator for the call."""
-    torch = _torch()
-    handle, context = _place(x, stream) if isinstance(x, torch.Tensor) else _matrix(x, "x", (), 0)
+    o = _once if _once.lib else _once.load()
+    context = _elsewhere(o, x, "x", stream)
+    if context is not None:
+        with context:
+            return linear_int8(x, w, w_scale, bias, out, out_dtype, workspace)
     device = x.get_device()
-    m, k, ldx = _matrix(x, "x", _T["floats"], device)
-    n, kw, ldw = _matrix(w, "w", (torch.int8,), device)
+    m, k, ldx = _matrix(o, x, "x", o.floats, device)
+    n, kw, ldw = _matrix(o, w, "w", o.int8s, device)
     if kw != k:
         raise ValueError(f"x has rows of {k}, w rows of {kw}")
-    sw = _vector(w_scale, "w_scale", torch.float32, n, device)
-    pbias = None if bias is None else _vector(bias, "bias", torch.float32, n, device)
-
-    def call(lib, o, dt, ldo):
-        need = lib.rt_linear_int8_workspace(m, k)
-        if workspace is not None:
-            ws, have = _workspace(workspace, device)
-        elif need > 0:
-            keep = torch.empty(need, dtype=torch.uint8, device=x.device)
-            ws, have = keep.data_ptr(), need
-        else:
-            ws, have = None, 0
-        return lib.rt_linear_int8(x.data_ptr(), _T["floats"][x.dtype], ldx, w.data_ptr(), ldw, sw, pbias, o, dt, ldo,
-                                  m, n, k, ws, have, handle)
-
-    out, st = _product(context, out, out_dtype or x.dtype, m, n, x.device, device, call)
+    sw = _vector(o, w_scale, "w_scale", o.fp32, n, device)
+    pbias = None if bias is None else _vector(o, bias, "bias", o.fp32, n, device)
+    out, code, ldo = _output(o, out, out_dtype or x.dtype, m, n, x, device)
+    lib = o.lib
+    if workspace is not None:
+        ws, have = _workspace(o, workspace, device)
+    else:
+        ws, have = None, lib.rt_linear_int8_workspace(m, n, k)
+        if have > 0:
+            workspace = o.empty(have, dtype=o.uint8, device=x.device)
+            ws = workspace.data_ptr()
+    st = lib.rt_linear_int8(x.data_ptr(), o.floats[x.dtype], ldx, w.data_ptr(), ldw, sw, pbias, out.data_ptr(), code,
+                            ldo, m, n, k, ws, have, o.stream(device))
     if st:
-        _raise(st, "linear_int8")
+        raise _lib.ResidentTopKError(st, "linear_int8")
     return out
 
 
-def linear_int8_workspace(m, k):
-    """Bytes of workspace linear_int8 needs for m activations of depth k."""
-    need = _lib.load().rt_linear_int8_workspace(int(m), int(k))
+def linear_int8_workspace(m, n, k):
+    """Bytes of workspace linear_int8 needs for m activations of depth k and n rows."""
+    need = _lib.load().rt_linear_int8_workspace(int(m), int(n), int(k))
     if need < 0:
-        _raise(_lib.RT_EINVAL, "linear_int8_workspace")
+        raise _lib.ResidentTopKError(_lib.RT_EINVAL, "linear_int8_workspace")
     return need
 
 
@@ -212,16 +222,8 @@ def sample_rows_workspace(r, v):
     """Bytes of workspace sample_rows needs for r rows of v logits."""
     need = _lib.load().rt_sample_rows_workspace(int(r), int(v))
     if need < 0:
-        _raise(_lib.RT_EINVAL, "sample_rows_workspace")
+        raise _lib.ResidentTopKError(_lib.RT_EINVAL, "sample_rows_workspace")
     return need
-
-
-def _workspace(t, device):
-    if not isinstance(t, _T["torch"].Tensor) or t.dtype != _T["torch"].uint8 or not t.is_contiguous():
-        raise TypeError("workspace must be a contiguous uint8 tensor")
-    if t.get_device() != device:
-        raise ValueError(f"workspace is on {t.device}, the call on cuda:{device}")
-    return t.data_ptr(), t.numel()
 
 
 def sample_rows(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, out_token=None, out_prob=None,
@@ -240,44 +242,51 @@ def sample_rows(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, out_t
 
     Returns (token int32 [r], prob fp32 [r], the drawn token's share of the kept
     weight); -1 and 0 for a row with no logit above -inf."""
-    torch = _torch()
-    handle, context = _place(logits, stream) if isinstance(logits, torch.Tensor) else _matrix(logits, "logits", (), 0)
+    o = _once if _once.lib else _once.load()
+    context = _elsewhere(o, logits, "logits", stream)
+    if context is not None:
+        with context:
+            return sample_rows(logits, u, temperature, top_k, top_p, min_p, out_token, out_prob, workspace)
     device = logits.get_device()
-    r, v, ld = _matrix(logits, "logits", _T["floats"], device)
-    pu = _vector(u, "u", torch.float32, r, device)
-    s = SampleSettings()
-    tensor = torch.Tensor
+    r, v, ld = _matrix(o, logits, "logits", o.floats, device)
+    pu = _vector(o, u, "u", o.fp32, r, device)
+    s, tensor = SampleSettings(), o.tensor
     if isinstance(temperature, tensor):
-        s.temperatures = _vector(temperature, "temperature", torch.float32, r, device)
+        s.temperatures = _vector(o, temperature, "temperature", o.fp32, r, device)
     else:
         s.temperature = temperature
     if isinstance(top_k, tensor):
-        s.top_ks = _vector(top_k, "top_k", torch.int32, r, device)
+        s.top_ks = _vector(o, top_k, "top_k", o.int32, r, device)
     else:
         s.top_k = min(max(int(top_k), 0), 2147483647)
     if isinstance(top_p, tensor):
-        s.top_ps = _vector(top_p, "top_p", torch.float32, r, device)
+        s.top_ps = _vector(o, top_p, "top_p", o.fp32, r, device)
     else:
         s.top_p = top_p
     if isinstance(min_p, tensor):
-        s.min_ps = _vector(min_p, "min_p", torch.float32, r, device)
+        s.min_ps = _vector(o, min_p, "min_p", o.fp32, r, device)
     else:
         s.min_p = min_p
-    with context or contextlib.nullcontext():
-        lib = _lib.load()
-        if out_token is None:
-            out_token = torch.empty(r, dtype=torch.int32, device=logits.device)
-        if out_prob is None:
-            out_prob = torch.empty(r, dtype=torch.float32, device=logits.device)
-        if workspace is not None:
-            ws, have = _workspace(workspace, device)
-        else:
-            have = lib.rt_sample_rows_workspace(r, v)
-            keep = torch.empty(have, dtype=torch.uint8, device=logits.device) if have > 0 else None
-            ws = keep.data_ptr() if have > 0 else None
-        st = lib.rt_sample_rows(logits.data_ptr(), _T["floats"][logits.dtype], r, v, ld, pu, ctypes.byref(s),
-                                _vector(out_token, "out_token", torch.int32, r, device),
-                                _vector(out_prob, "out_prob", torch.float32, r, device), ws, have, handle)
+    if out_token is None:
+        out_token = o.empty(r, dtype=o.int32, device=logits.device)
+        ptoken = out_token.data_ptr()
+    else:
+        ptoken = _vector(o, out_token, "out_token", o.int32, r, device)
+    if out_prob is None:
+        out_prob = o.empty(r, dtype=o.fp32, device=logits.device)
+        pprob = out_prob.data_ptr()
+    else:
+        pprob = _vector(o, out_prob, "out_prob", o.fp32, r, device)
+    lib = o.lib
+    if workspace is not None:
+        ws, have = _workspace(o, workspace, device)
+    else:
+        ws, have = None, lib.rt_sample_rows_workspace(r, v)
+        if have > 0:
+            workspace = o.empty(have, dtype=o.uint8, device=logits.device)
+            ws = workspace.data_ptr()
+    st = lib.rt_sample_rows(logits.data_ptr(), o.floats[logits.dtype], r, v, ld, pu, ctypes.byref(s), ptoken, pprob,
+                            ws, have, o.stream(device))
     if st:
-        _raise(st, "sample_rows")
+        raise _lib.ResidentTopKError(st, "sample_rows")
     return out_token, out_prob
