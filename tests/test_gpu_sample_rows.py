@@ -61,23 +61,50 @@ def test_filters(dtype, v, f):
     check(x, u, **FILTERS[f])
 
 
-@pytest.mark.parametrize("dtype,v", [("bf16", 131072), ("fp32", 262145), ("fp16", 1000003)])
-@pytest.mark.parametrize("f", [0, 4, 7, 8, 9, 10])
-def test_long_rows(dtype, v, f):
-    x, u = logits(2, v, dtype, v + f)
+@pytest.mark.parametrize("dtype,v,r", [("bf16", 131072, 2), ("bf16", 131072, 20), ("fp32", 262145, 2), ("fp16", 1000003, 2),
+                                       ("fp32", 700001, 17)])
+@pytest.mark.parametrize("f", [0, 4, 6, 7, 8, 9, 10])
+def test_long_rows(dtype, v, r, f):
+    x, u = logits(r, v, dtype, v + f)
     check(x, u, **FILTERS[f])
 
 
+def test_long_rows_of_every_kind_at_once():
+    """Shared rows (several workgroups each): empty, one token, greedy, infinite, tied, masked and flat rows
+    with settings of their own, in one call; then each with no filter, top-p, min-p and top-k for all."""
+    r, v = 8, 150000
+    g = torch.Generator().manual_seed(30)
+    x = torch.randn(r, v, generator=g)
+    x[0] = -INF
+    x[1] = NAN
+    x[1, 140001] = 0.5
+    x[2, ::2] = -INF
+    x[3, [7, 77777, 149999]] = INF
+    x[4] = 2.0
+    x[5] = torch.randint(-4, 5, (v,), generator=g).float()
+    x[6] = torch.finfo(torch.float32).min
+    x[6, 99999] = 1.0
+    u = torch.rand(r, generator=g)
+    check(x, u, exact_ties=True, temperature=torch.tensor([1.0, 1.0, 0.0, 1.0, 1.0, 0.9, 1.0, 2.0]),
+          top_k=torch.tensor([0, 50, 0, 2, 30000, 0, 9, 5000], dtype=torch.int32),
+          top_p=torch.tensor([0.9, 0.5, 1.0, 1.0, 1.0, 0.7, 0.9, 0.95]),
+          min_p=torch.tensor([0.0, 0.1, 0.0, 0.0, 0.0, 0.0, 0.01, 0.0]))
+    for s in (dict(), dict(top_p=0.9), dict(min_p=0.2), dict(top_k=10), dict(top_k=40000, top_p=0.5), dict(temperature=0.0)):
+        check(x, u, exact_ties=True, **s)
+
+
 @pytest.mark.parametrize("dtype", list(TYPES))
-def test_settings_of_each_row(dtype):
-    r = 40
-    x, u = logits(r, 3001, dtype, 77)
+@pytest.mark.parametrize("r,v", [(40, 3001), (9, 200001), (3, 300000)])
+def test_settings_of_each_row(dtype, r, v):
+    x, u = logits(r, v, dtype, 77 + r)
     g = torch.Generator().manual_seed(8)
 
     def pick(values, dt):
         return torch.tensor(values, dtype=dt)[torch.randint(0, len(values), (r,), generator=g)]
 
-    check(x, u, temperature=pick([0.0, 0.5, 1.0, 2.0, -1.0], torch.float32),
+    # bf16 and fp16 rows this long hold their largest logit more than once: top_p 0.5 and min_p 1 then
+    # meet exact ties, which whole weights decide as the definition does
+    check(x, u, exact_ties=True, temperature=pick([0.0, 0.5, 1.0, 2.0, -1.0], torch.float32),
           top_k=pick([0, 1, 2, 50, 2000, 5000, -3], torch.int32),
           top_p=pick([1.0, 0.5, 0.9, 0.0, 2.0], torch.float32), min_p=pick([0.0, 0.1, 0.001, 1.0], torch.float32))
 

@@ -39,6 +39,7 @@ constexpr int kWaves = kThreads / 64;
 constexpr int kList = 2048;   // candidates kept in LDS
 constexpr int kSmall = 128;   // lists up to here are settled by comparing all pairs
 constexpr int kSegs = 8;      // parts of a row with a histogram each
+constexpr int kSlices = kSampleSlices;  // most workgroups that share a row
 constexpr int kSearch = 2048; // bins of find_first, two per thread
 constexpr int kPlaces = 4096; // 16-byte places that hold candidates
 
@@ -189,7 +190,7 @@ struct Shared {
     uint64_t list[kList];
     uint64_t weight[kSmall];
     double factor[kMass];
-    uint64_t seg[kSegs];
+    uint64_t seg[kSlices];
     uint64_t wave_sum[kWaves];
     uint64_t lo, hi, before;
     uint32_t count, found;
@@ -380,11 +381,12 @@ struct Row {
     static constexpr int64_t kChunk = int64_t(kThreads) * E;
     const T *p;
     int64_t v;
-    int chunks, per;  // chunks of the row, and of each eighth of it
+    int begin, end, per;  // the chunks that the passes below go over, and how many make a segment
 
     __device__ __forceinline__ Row(const SampleArgs &a, int64_t r) : p(static_cast<const T *>(a.logits) + r * a.ld), v(a.v) {
-        chunks = int((v + kChunk - 1) / kChunk);
-        per = (chunks + kSegs - 1) / kSegs;
+        begin = 0;
+        end = int((v + kChunk - 1) / kChunk);
+        per = (end + kSegs - 1) / kSegs;
     }
     __device__ __forceinline__ uint32_t index(int c, uint32_t t = threadIdx.x) const {
         return uint32_t(c) * uint32_t(kChunk) + t * E;
@@ -425,12 +427,13 @@ struct Row {
     __device__ __forceinline__ u32x4 load(int64_t c, uint32_t t = threadIdx.x) const {
         return (c + 1) * kChunk <= v ? load_whole(c, t) : load_last(c, t);
     }
-    // f(16 bytes, chunk) over chunks c .. c1 - 1.  Two chunks are read while two are
+    // f(16 bytes, chunk) over the row's chunks.  Two chunks are read while two are
     // worked on: the registers are named apart, since handing a load on from one
     // to the next would wait for it.
     template <typename F>
-    __device__ __forceinline__ void each_chunk(F f, int c, int c1) const {
-        const int whole = min(c1, int(v / kChunk)), last = whole - 1;
+    __device__ __forceinline__ void each_chunk(F f) const {
+        const int whole = min(end, int(v / kChunk)), last = whole - 1;
+        int c = begin;
         if (c + 4 <= whole) {
             u32x4 a0 = load_whole(c), a1 = load_whole(c + 1);
 #pragma unroll 1
@@ -445,7 +448,7 @@ struct Row {
             }
         }
 #pragma unroll 1
-        for (; c < c1; ++c) f(load(c), c);
+        for (; c < end; ++c) f(load(c), c);
     }
     // f(value, index) of each element of chunks c .. c1 - 1, one chunk at a time: for
     // the rarely taken paths, where small code matters more
@@ -461,7 +464,7 @@ struct Row {
     }
     template <typename F>
     __device__ __forceinline__ void each(F f) const {
-        each(f, 0, chunks);
+        each(f, begin, end);
     }
     static __device__ __forceinline__ float largest(u32x4 x) {  // -inf for NaN
         float m = -INFINITY;
@@ -505,8 +508,7 @@ struct Row {
                     const uint32_t at = atomicAdd(&sh.found, 1u);
                     if (at < kPlaces) places[at] = uint32_t(c) * kThreads + threadIdx.x;
                 }
-            },
-            0, chunks);
+            });
         __syncthreads();
         const uint32_t n = sh.found;
         if (n > kPlaces) return kList + 1;
@@ -529,7 +531,7 @@ struct Row {
         const uint32_t n = sh.found;
         for (uint32_t h = threadIdx.x >> 6; h < n; h += kWaves) {
             const uint32_t t = threads[h];
-            for (int c = threadIdx.x & 63; c < chunks; c += 64) {
+            for (int c = begin + (threadIdx.x & 63); c < end; c += 64) {
                 take(sh, load(c, t), index(c, t), lo, INFINITY);
             }
         }
@@ -771,21 +773,20 @@ __device__ __forceinline__ Pair pairs_of_list(Shared &sh, uint32_t n, const Weig
     return p;
 }
 
-// The draw once the eighths' kept weights are in sh.seg: the element of the
+// The draw once the segments' kept weights are in sh.seg: the element of the
 // row at which the running weight of what `cut` keeps reaches above(u, sum).
 template <typename T>
 __device__ __forceinline__ void draw_from_row(Shared &sh, Output out, int64_t r, const Row<T> &row,
                                               const Weights &weight, float u, const Cut &cut) {
     uint64_t sum = 0;
-#pragma unroll
-    for (int s = 0; s < kSegs; ++s) sum += sh.seg[s];
-    uint64_t target = above(u, sum);
     int seg = 0, last = 0;
-#pragma unroll
-    for (int s = 0; s < kSegs; ++s)
+    for (int s = 0; s < kSlices; ++s) {
+        sum += sh.seg[s];
         if (sh.seg[s]) last = s;
+    }
+    uint64_t target = above(u, sum);
     while (seg < last && sh.seg[seg] < target) target -= sh.seg[seg++];
-    const int end = min((seg + 1) * row.per, row.chunks);
+    const int end = min((seg + 1) * row.per, row.end);
     for (int c = seg * row.per; c < end; ++c) {
         const u32x4 x = row.load(c);
         const uint32_t i = row.index(c);
@@ -838,15 +839,15 @@ template <typename T>
 __device__ __forceinline__ void draw_by_cut(Shared &sh, Output out, int64_t r, Row<T> row, Weights weight, float u,
                                          Cut cut) {
     __syncthreads();
-    if (threadIdx.x < kSegs) sh.seg[threadIdx.x] = 0;
+    if (threadIdx.x < kSlices) sh.seg[threadIdx.x] = 0;
     __syncthreads();
-    for (int s = 0; s < kSegs && s * row.per < row.chunks; ++s) {
+    for (int s = 0; s * row.per < row.end; ++s) {
         uint64_t sum = 0;
         row.each(
             [&](float y, uint32_t i) {
                 if (cut(y, i)) sum += weight(y);
             },
-            s * row.per, min((s + 1) * row.per, row.chunks));
+            s * row.per, min((s + 1) * row.per, row.end));
         sum = wave_add(sum);
         if ((threadIdx.x & 63) == 0 && sum) add64(&sh.seg[s], sum);
     }
@@ -900,9 +901,9 @@ __device__ __forceinline__ float bin_edge(const Weights &weight, float top, int 
 }
 
 // The histograms of the weights of what `inside` keeps.
-template <typename T, typename Inside>
+template <int SEGS, typename T, typename Inside>
 __device__ __forceinline__ void mass_histogram(Shared &sh, const Row<T> &row, const Weights &weight, Inside inside) {
-    for (int i = threadIdx.x; i < kSegs * kStride; i += kThreads) sh.bin[i] = 0;
+    for (int i = threadIdx.x; i < SEGS * kStride; i += kThreads) sh.bin[i] = 0;
     __syncthreads();
     // bin b of a segment is at [kMass - 1 - b]
     const int spread = kMass - (kMass - 1) + int(threadIdx.x & 63);
@@ -926,9 +927,96 @@ __device__ __forceinline__ void mass_histogram(Shared &sh, const Row<T> &row, co
                 }
             }
             if (--left == 0) bins += kStride, left = row.per;
-        },
-        0, row.chunks);
+        });
     __syncthreads();
+}
+
+__device__ __forceinline__ Weights weights_of(Shared &sh, const SampleArgs &args, float top, float temperature) {
+    return Weights{double(top), 1.4426950408889634 / kOctaves / double(temperature),
+                   (lds_doubles)(sh.factor + kMass - 1), args.c4, args.c3, args.c2, args.c1, args.one, args.per_unit};
+}
+
+// The factors' table; a barrier follows before its first use.
+__device__ __forceinline__ void fill_factors(Shared &sh, int shift) {
+    for (int b = threadIdx.x; b < kMass; b += kThreads)
+        sh.factor[kMass - 1 - b] =
+            b < kMass - 1 ? __builtin_ldexp(exp2(double(b % kPerOctave) / -kPerOctave), shift - b / kPerOctave) : 0.0;
+}
+
+// Counts x, at least floor, in the bins of [floor, top].
+__device__ __forceinline__ void count_logit(Shared &sh, float x, float top, float scale) {
+    add64(&sh.bin[min(int(fminf((top - x) * scale, float(kSearch))), kSearch - 1)], 1);
+}
+__device__ __forceinline__ float count_scale(float top, float floor) {
+    return fminf(float(kSearch - 1) / (top - floor), 1e30f);
+}
+// The lower edge of the bin where that count reaches k (-inf where it does not
+// at all): at least k of what was counted reach it.  All threads; after a barrier.
+__device__ __forceinline__ float count_edge(Shared &sh, int32_t k, float top, float floor, float scale) {
+    uint64_t before, target, all = 0;
+    const int last = find_bin(sh, sh.bin[2 * threadIdx.x], sh.bin[2 * threadIdx.x + 1],
+                              [&](uint64_t sum) { all = sum; return uint64_t(k); }, &before, &target);
+    if (all < uint64_t(k)) return -INFINITY;
+    // the roundings of a bin are far below 2^-20 of its distance and 2^-22 of top
+    return fmaxf(top - float(last + 1) / scale * 1.000001f - fabsf(top) * 2.4e-7f, floor);
+}
+
+// The bin that the border cuts, top-p's or min-p's where that comes first (kMass:
+// none, or one without weight), from this thread's bins 2 t and 2 t + 1 over the
+// whole row (only looked at where top-p is on).
+struct Border {
+    int bin;
+    bool by_p;                // top-p's border lies in it, at weight target - before within it
+    uint64_t before, target;
+};
+__device__ __forceinline__ Border find_border(Shared &sh, const Weights &weight, const Settings &set, float least,
+                                              uint64_t b0, uint64_t b1) {
+    Border border{kMass, false, 0, 0};
+    if (set.top_p < 1.0f) {
+        const int bin = 2 * threadIdx.x;
+        if (bin < kMass - 1) b0 = weight.whole(b0, bin), b1 = weight.whole(b1, bin + 1);
+        border.bin = find_bin(sh, b0, b1, [&](uint64_t all) { return at_least(set.top_p, all); }, &border.before,
+                              &border.target);
+        border.by_p = true;
+    }
+    if (least > -INFINITY) {
+        double f;
+        const int l = -weight.split(least, &f);
+        if (l < border.bin) border.by_p = false, border.bin = l;
+    }
+    if (border.bin >= kMass - 1) border.bin = kMass, border.by_p = false;
+    return border;
+}
+
+// The edges of bin b in sh.edge: logits from [0] on and below [1].  A barrier follows.
+__device__ __forceinline__ void find_edges(Shared &sh, const Weights &weight, float top, int b) {
+    const int wave = threadIdx.x >> 6;
+    if (wave < 2) {
+        const float e = b - wave >= 0 ? bin_edge(weight, top, b - wave) : INFINITY;
+        if ((threadIdx.x & 63) == 0) sh.edge[wave] = e;
+    }
+}
+
+// Puts the border among sh.list[0, n), the elements of its bin (logits in [lo, hi]), into
+// `cut`, and the weights of those it keeps onto their segments'.
+template <typename T>
+__device__ __forceinline__ void settle_list(Shared &sh, const Row<T> &row, const Weights &weight, uint32_t n,
+                                            const Border &border, float lo, float hi, float least, Cut &cut) {
+    const Pair p = pairs_of_list(sh, n, weight);
+    if (border.by_p) {
+        uint64_t key;
+        if (find_in_pairs(sh, p, n, uint64_t(ordered(lo)) << 32, (uint64_t(ordered(hi)) << 32) | 0xffffffffu,
+                          border.target - border.before, &key))
+            sh.before = key;
+        __syncthreads();
+        key = sh.before;
+        if (key) cut.from_key(key);  // else the bin's weights all round to 0: what it holds cannot be drawn
+    }
+    cut.from_value(least);
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+        if (p.weight[e] && cut(key_value(p.key[e]), key_index(p.key[e])))
+            add64(&sh.seg[row.segment(key_index(p.key[e]))], p.weight[e]);
 }
 
 // One row by one workgroup.
@@ -948,8 +1036,7 @@ __device__ __forceinline__ void sample_row(Shared &sh, const SampleArgs &args, i
 #pragma unroll
             for (int g = 0; g < 4; ++g)
                 if ((c & 3) == g) own[g] = m > own[g] ? m : own[g];
-        },
-        0, row.chunks);
+        });
     const float mine = fmaxf(fmaxf(own[0], own[1]), fmaxf(own[2], own[3]));
     float top = mine, floor = INFINITY;
 #pragma unroll
@@ -980,9 +1067,7 @@ __device__ __forceinline__ void sample_row(Shared &sh, const SampleArgs &args, i
     }
     if (top == INFINITY) return draw_infinite(sh, out, r, row, set);
 
-    const Weights weight{double(top), 1.4426950408889634 / kOctaves / double(set.temperature),
-                         (lds_doubles)(sh.factor + kMass - 1), args.c4, args.c3, args.c2, args.c1, args.one,
-                         args.per_unit};
+    const Weights weight = weights_of(sh, args, top, set.temperature);
     const float least = set.least(top);
     const auto value = [&](uint32_t i) { return static_cast<float>(row.p[i]); };
     if (row.v <= kList) {
@@ -994,20 +1079,14 @@ __device__ __forceinline__ void sample_row(Shared &sh, const SampleArgs &args, i
         // A value that at least k elements reach, and few more: the lower edge of the
         // bin where the count of those 4096 largest logits reaches k (of 4096, one
         // seldom hides another of the first k).
-        const float scale = fminf(float(kSearch - 1) / (top - floor), 1e30f);
         if (set.top_k <= kThreads && floor < top) {
+            const float scale = count_scale(top, floor);
 #pragma unroll
             for (int g = 0; g < 4; ++g)
-                if (own[g] > -INFINITY)
-                    add64(&sh.bin[min(int(fminf((top - own[g]) * scale, float(kSearch))), kSearch - 1)], 1);
+                if (own[g] > -INFINITY) count_logit(sh, own[g], top, scale);
             __syncthreads();
-            uint64_t before, target, all = 0;
-            const int last = find_bin(sh, sh.bin[2 * t], sh.bin[2 * t + 1],
-                                      [&](uint64_t sum) { all = sum; return uint64_t(set.top_k); }, &before, &target);
-            if (all >= uint64_t(set.top_k)) {
-                // the roundings of a bin are far below 2^-20 of its distance and 2^-22 of top
-                const float edge = top - float(last + 1) / scale * 1.000001f - fabsf(top) * 2.4e-7f;
-                const float from = fmaxf(edge, floor);
+            const float from = count_edge(sh, set.top_k, top, floor, scale);
+            if (from > -INFINITY) {
                 // a wave takes about as long for one thread's place as for 64 threads' chunk
                 const uint32_t n = set.top_k <= 128 ? row.collect_from(sh, from, mine)
                                                     : row.template collect<false>(sh, from, INFINITY);
@@ -1020,29 +1099,17 @@ __device__ __forceinline__ void sample_row(Shared &sh, const SampleArgs &args, i
 
     const bool cut_k = set.top_k != 0;
     if (cut_k)
-        mass_histogram(sh, row, weight, cut);
+        mass_histogram<kSegs>(sh, row, weight, cut);
     else
-        mass_histogram(sh, row, weight, [](float, uint32_t) { return true; });
-    // the bin that the border cuts: top-p's, or min-p's where it comes first
-    uint64_t before = 0, target = 0;
-    int b = kMass;
-    if (set.top_p < 1.0f) {
-        uint64_t b0 = 0, b1 = 0;
-        if (2 * t < kMass - 1) {
+        mass_histogram<kSegs>(sh, row, weight, [](float, uint32_t) { return true; });
+    uint64_t b0 = 0, b1 = 0;
+    if (set.top_p < 1.0f && 2 * t < kMass - 1) {
 #pragma unroll
-            for (int s = 0; s < kSegs; ++s) b0 += sh.bin[s * kStride + kMass - 1 - 2 * t], b1 += sh.bin[s * kStride + kMass - 2 - 2 * t];
-            b0 = weight.whole(b0, 2 * t);
-            b1 = weight.whole(b1, 2 * t + 1);
-        }
-        b = find_bin(sh, b0, b1, [&](uint64_t all) { return at_least(set.top_p, all); }, &before, &target);
+        for (int s = 0; s < kSegs; ++s)
+            b0 += sh.bin[s * kStride + kMass - 1 - 2 * t], b1 += sh.bin[s * kStride + kMass - 2 - 2 * t];
     }
-    bool by_p = b < kMass;
-    if (least > -INFINITY) {
-        double f;
-        const int l = -weight.split(least, &f);
-        if (l < b) by_p = false, b = l;
-    }
-    if (b >= kMass - 1) b = kMass;  // the border lies among elements without weight, or there is none
+    const Border border = find_border(sh, weight, set, least, b0, b1);
+    const int b = border.bin;
     // about how many elements bin b holds, and the weights kept whole, by eighth
     uint64_t in_bin = 0;
     if (b < kMass) {
@@ -1050,7 +1117,7 @@ __device__ __forceinline__ void sample_row(Shared &sh, const SampleArgs &args, i
         for (int s = 0; s < kSegs; ++s) in_bin += sh.bin[s * kStride + kMass - 1 - b];
         in_bin >>= args.shift;
     }
-    if (t < kSegs) sh.seg[t] = 0;
+    if (t < kSlices) sh.seg[t] = 0;
     __syncthreads();
     {
         // 128 threads an eighth, a bin in 128 each, summed in 64-bit floating point in a fixed order
@@ -1063,35 +1130,17 @@ __device__ __forceinline__ void sample_row(Shared &sh, const SampleArgs &args, i
         if ((t & 63) == 0) add64(&sh.seg[s], all);
     }
     if (b < kMass) {
-        if (t < 128) {
-            const int at = b - (t >> 6);
-            const float e = at >= 0 ? bin_edge(weight, top, at) : INFINITY;
-            if ((t & 63) == 0) sh.edge[t >> 6] = e;
-        }
+        find_edges(sh, weight, top, b);
         __syncthreads();
         const float lo = sh.edge[0], hi = sh.edge[1];
         const uint32_t n = cut_k || in_bin > 2 * kList ? kList + 1 : row.template collect<true>(sh, lo, hi);
         if (n > kList) {
-            if (by_p)
-                cut.from_key(border_in_row<T>(sh, row, true, weight, lo, hi, cut, target - before));
+            if (border.by_p)
+                cut.from_key(border_in_row<T>(sh, row, true, weight, lo, hi, cut, border.target - border.before));
             cut.from_value(least);
             return draw_by_cut(sh, out, r, row, weight, set.u, cut);
         }
-        const Pair p = pairs_of_list(sh, n, weight);
-        if (by_p) {
-            uint64_t key;
-            if (find_in_pairs(sh, p, n, uint64_t(ordered(lo)) << 32, (uint64_t(ordered(fminf(hi, top))) << 32) | 0xffffffffu,
-                              target - before, &key))
-                sh.before = key;
-            __syncthreads();
-            key = sh.before;
-            if (key) cut.from_key(key);  // else the bin's weights all round to 0: what it holds cannot be drawn
-        }
-        cut.from_value(least);
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-            if (p.weight[e] && cut(key_value(p.key[e]), key_index(p.key[e])))
-                add64(&sh.seg[row.segment(key_index(p.key[e]))], p.weight[e]);
+        settle_list(sh, row, weight, n, border, lo, fminf(hi, top), least, cut);
     }
     __syncthreads();
     draw_from_row(sh, out, r, row, weight, set.u, cut);
@@ -1101,14 +1150,287 @@ template <typename T>
 __global__ __launch_bounds__(kThreads) void row_kernel(SampleArgs args, int64_t first) {
     extern __shared__ __align__(16) char memory[];
     Shared &sh = *reinterpret_cast<Shared *>(memory);
-    for (int b = threadIdx.x; b < kMass; b += kThreads)
-        sh.factor[kMass - 1 - b] =
-            b < kMass - 1 ? __builtin_ldexp(exp2(double(b % kPerOctave) / -kPerOctave), args.shift - b / kPerOctave) : 0.0;
+    fill_factors(sh, args.shift);
     sample_row<T>(sh, args, first + blockIdx.x);  // its first barrier is ahead of the factors' first use
 }
 
+// ------------------------------------------------------- few rows, long ones
+
+// A few long rows leave most CUs idle with one workgroup a row: there, `slices`
+// workgroups share a row, in four kernels over a workspace (each starts where
+// the last has ended: nothing waits inside a kernel):
+//   1. each slice's largest logit, and its threads' largest;
+//   2. top-k: the value that k of all threads' largest reach, and the slice's
+//      elements from it on; else the slice's histogram;
+//   3. (not for top-k) the whole row's histogram, the border's bin, the slice's
+//      elements of it and its weight before it;
+//   4. one workgroup a row: the slices' lists as one, the border, the draw.
+struct Slice {
+    float top, floor;
+    uint32_t first;    // the lowest index that holds `top`
+    uint32_t count;    // of list; above kList: the row goes the one-workgroup way
+    uint64_t kept;     // weight before the border's bin
+    float lo, hi;      // edges of that bin (in the first slice)
+    Border border;     // (in the first slice)
+    float own[kThreads];       // each thread's largest logit
+    alignas(16) uint64_t mass[kMass + 1];  // the histogram, bin 0 first
+    uint64_t list[kList];
+};
+
 template <typename T>
-hipError_t launch(const SampleArgs &a, hipStream_t s) {
+struct SliceOf {
+    Row<T> row;
+    Slice *all, *own;  // the row's slices, this one
+    int slices;
+    float top, floor;
+
+    __device__ __forceinline__ SliceOf(const SampleArgs &a, Slice *work, int64_t r, int s, int n, int per)
+        : row(a, r), all(work + r * n), own(work + r * n + s), slices(n) {
+        row.per = per;
+        row.begin = s * per;
+        row.end = min(row.begin + per, row.end);
+    }
+    // use(load(slice)) for each of the row's slices, `none` for a missing one: the
+    // loads of eight at a time, since one after the other costs a round trip each.
+    template <typename Load, typename V, typename Use>
+    __device__ __forceinline__ void each_slice(Load load, V none, Use use) const {
+        for (int s = 0; s < slices; s += 8) {
+            V v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = s + i < slices ? load(all[min(s + i, slices - 1)]) : none;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) use(v[i]);
+        }
+    }
+    // The row's largest logit and the smallest of its threads' largest (32 slices at most).
+    __device__ __forceinline__ void extremes() {
+        const int lane = threadIdx.x & 63;
+        top = wave_max(lane < slices ? all[lane].top : -INFINITY);
+        floor = wave_min(lane < slices ? all[lane].floor : INFINITY);
+    }
+};
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void split_top_kernel(SampleArgs args, Slice *work, int slices, int per) {
+    extern __shared__ __align__(16) char memory[];
+    Shared &sh = *reinterpret_cast<Shared *>(memory);
+    const int t = threadIdx.x;
+    SliceOf<T> slice(args, work, blockIdx.y, blockIdx.x, slices, per);
+    const Settings set(args, blockIdx.y);
+    float own = -INFINITY;
+    slice.row.each_chunk([&](u32x4 x, int) {
+        const float m = Row<T>::largest(x);
+        own = m > own ? m : own;
+    });
+    slice.own->own[t] = own;
+    float top = wave_max(own), floor = wave_min(own > -INFINITY ? own : INFINITY);
+    if ((t & 63) == 0) sh.f[t >> 6] = top, sh.g[t >> 6] = floor;
+    if (t == 0) sh.found = 0xffffffffu;
+    __syncthreads();
+    top = wave_max(sh.f[t & (kWaves - 1)]);
+    floor = wave_min(sh.g[t & (kWaves - 1)]);
+    if (set.single && top > -INFINITY) {
+        if (own == top) {
+            uint32_t first = 0xffffffffu;
+            slice.row.each([&](float x, uint32_t i) {
+                if (x >= top && i < first) first = i;
+            });
+            atomicMin(&sh.found, first);
+        }
+        __syncthreads();
+    }
+    if (t == 0) {
+        slice.own->top = top;
+        slice.own->floor = floor;
+        slice.own->first = sh.found;
+        slice.own->count = 0;
+        slice.own->kept = 0;
+    }
+}
+
+// sh.list[0, n) to the slice's own.
+__device__ __forceinline__ void write_list(Shared &sh, Slice *own, uint32_t n) {
+    for (uint32_t j = threadIdx.x; j < min(n, uint32_t(kList)); j += kThreads) own->list[j] = sh.list[j];
+    if (threadIdx.x == 0) own->count = n;
+}
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void split_candidates_kernel(SampleArgs args, Slice *work, int slices, int per) {
+    extern __shared__ __align__(16) char memory[];
+    Shared &sh = *reinterpret_cast<Shared *>(memory);
+    const int t = threadIdx.x;
+    SliceOf<T> slice(args, work, blockIdx.y, blockIdx.x, slices, per);
+    const Settings set(args, blockIdx.y);
+    slice.extremes();
+    const float top = slice.top, floor = slice.floor;
+    if (set.single || !(fabsf(top) < INFINITY)) return;
+    if (set.top_k) {
+        float from = -INFINITY;
+        if (set.top_k <= kThreads && floor < top) {
+            for (int i = t; i < kSearch; i += kThreads) sh.bin[i] = 0;
+            __syncthreads();
+            const float scale = count_scale(top, floor);
+            slice.each_slice([&](const Slice &one) { return one.own[t]; }, -INFINITY, [&](float x) {
+                if (x > -INFINITY) count_logit(sh, x, top, scale);
+            });
+            __syncthreads();
+            from = count_edge(sh, set.top_k, top, floor, scale);
+        }
+        uint32_t n = kList + 1;
+        if (from > -INFINITY) n = slice.row.template collect<false>(sh, from, INFINITY);
+        return write_list(sh, slice.own, n);
+    }
+    const Weights weight = weights_of(sh, args, top, set.temperature);  // no factor is read
+    mass_histogram<1>(sh, slice.row, weight, [](float, uint32_t) { return true; });
+    for (int b = t; b < kMass; b += kThreads) slice.own->mass[b] = sh.bin[kMass - 1 - b];
+}
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void split_border_kernel(SampleArgs args, Slice *work, int slices, int per) {
+    extern __shared__ __align__(16) char memory[];
+    Shared &sh = *reinterpret_cast<Shared *>(memory);
+    const int t = threadIdx.x;
+    SliceOf<T> slice(args, work, blockIdx.y, blockIdx.x, slices, per);
+    const Settings set(args, blockIdx.y);
+    slice.extremes();
+    const float top = slice.top;
+    if (set.single || set.top_k || !(fabsf(top) < INFINITY)) return;
+    fill_factors(sh, args.shift);
+    __syncthreads();
+    const Weights weight = weights_of(sh, args, top, set.temperature);
+    const float least = set.least(top);
+    uint64_t b0 = 0, b1 = 0;
+    if (set.top_p < 1.0f && 2 * t < kMass - 1) {
+        typedef uint64_t u64x2 __attribute__((ext_vector_type(2)));
+        slice.each_slice([&](const Slice &one) { return *reinterpret_cast<const u64x2 *>(one.mass + 2 * t); }, u64x2{0, 0},
+                         [&](u64x2 m) { b0 += m[0], b1 += m[1]; });
+    }
+    const Border border = find_border(sh, weight, set, least, b0, b1);
+    double sum = 0.0;  // in a fixed order: 64-bit floating point is as good as whole numbers
+    for (int b = t; b < min(border.bin, kMass - 1); b += kThreads)
+        sum = fma(double(slice.own->mass[b]), weight.zero[-b] * weight.per_unit, sum);
+    const uint64_t kept = block_add(sh, uint64_t(__builtin_rint(sum)));
+    if (border.bin < kMass) {
+        find_edges(sh, weight, top, border.bin);
+        __syncthreads();
+        const float lo = sh.edge[0], hi = sh.edge[1];
+        write_list(sh, slice.own, slice.row.template collect<true>(sh, lo, hi));
+        if (t == 0) slice.own->lo = lo, slice.own->hi = fminf(hi, top);
+    }
+    if (t == 0) {
+        slice.own->kept = kept;
+        slice.own->border = border;
+    }
+}
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void split_draw_kernel(SampleArgs args, Slice *work, int slices, int per) {
+    extern __shared__ __align__(16) char memory[];
+    Shared &sh = *reinterpret_cast<Shared *>(memory);
+    const int t = threadIdx.x;
+    const int64_t r = blockIdx.x;
+    SliceOf<T> slice(args, work, r, 0, slices, per);
+    const Settings set(args, r);
+    const Output out{args.out_token, args.out_prob};
+    slice.extremes();
+    const float top = slice.top;
+    if (top == -INFINITY) {
+        if (t == 0) write_row(out, r, 0xffffffffu, 0.0f);
+        return;
+    }
+    if (set.single) {
+        uint32_t first = 0xffffffffu;
+        if ((t & 63) < slices && slice.all[t & 63].top == top) first = slice.all[t & 63].first;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) first = min(first, uint32_t(__shfl_xor(int(first), o)));
+        if (t == 0) write_row(out, r, first, 1.0f);
+        return;
+    }
+    fill_factors(sh, args.shift);
+    // the slices' lists side by side
+    const uint64_t upto = wave_scan((t & 63) < slices ? slice.all[t & 63].count : 0);
+    const uint64_t total = lane64(upto, 63);
+    const bool whole = !__any((t & 63) < slices && slice.all[t & 63].count > uint32_t(kList));
+    // (sample_row's first barrier is ahead of the factors' use)
+    if (!whole || (set.top_k && total > kList) || top == INFINITY) return sample_row<T>(sh, args, r);
+    const uint32_t n = uint32_t(total);
+    if (n <= kList) {
+        if (t < kSlices) sh.bin[t] = upto;
+        __syncthreads();
+        for (uint32_t j = t; j < n; j += kThreads) {
+            int s = 0;
+            while (sh.bin[s] <= j) ++s;
+            sh.list[j] = slice.all[s].list[j - (s ? uint32_t(sh.bin[s - 1]) : 0)];
+        }
+    }
+    if (t < kSlices) sh.seg[t] = t < slices ? slice.all[t].kept : 0;
+    __syncthreads();
+    Row<T> row(args, r);
+    row.per = per;
+    const Weights weight = weights_of(sh, args, top, set.temperature);
+    const float least = set.least(top);
+    if (set.top_k)
+        return draw_from_list(sh, out, r, n, weight, set, least, uint32_t(row.v),
+                              [&](uint32_t i) { return static_cast<float>(row.p[i]); });
+    Cut cut;
+    const Border border = slice.own->border;
+    if (border.bin < kMass && n <= kList) {
+        settle_list(sh, row, weight, n, border, slice.own->lo, slice.own->hi, least, cut);
+    } else if (border.bin < kMass) {  // more than LDS holds: from where they are
+        const auto lists = [&](auto f) {
+            for (int s = 0; s < slices; ++s) {
+                const uint32_t own = slice.all[s].count;
+                for (uint32_t j = t; j < own; j += kThreads) {
+                    const uint64_t key = slice.all[s].list[j];
+                    f(key, weight(key_value(key)));
+                }
+            }
+        };
+        if (border.by_p) {
+            const uint64_t key = find_first(sh, lists, border.target - border.before);
+            if (key) cut.from_key(key);
+        }
+        cut.from_value(least);
+        lists([&](uint64_t key, uint64_t w) {
+            if (cut(key_value(key), key_index(key))) add64(&sh.seg[row.segment(key_index(key))], w);
+        });
+    }
+    __syncthreads();
+    draw_from_row(sh, out, r, row, weight, set.u, cut);
+}
+
+template <typename T>
+hipError_t launch_split(const SampleArgs &a, Split split, void *workspace, hipStream_t s) {
+    Slice *work = static_cast<Slice *>(workspace);
+    static std::atomic<uint64_t> told[4];
+    void (*const kernels[4])(SampleArgs, Slice *, int, int) = {split_top_kernel<T>, split_candidates_kernel<T>,
+                                                               split_border_kernel<T>, split_draw_kernel<T>};
+    hipError_t err = hipSuccess;
+    for (int i = 0; i < 4 && err == hipSuccess; ++i) {
+        if (i == 2 && a.set.top_ks == nullptr && a.set.top_k > 0 && a.set.top_k < a.v) continue;  // every row is top-k's
+        err = allow_lds(reinterpret_cast<const void *>(kernels[i]), int(sizeof(Shared)), told[i]);
+        if (err != hipSuccess) break;
+        const dim3 grid = i == 3 ? dim3(unsigned(a.r)) : dim3(unsigned(split.slices), unsigned(a.r));
+        kernels[i]<<<grid, kThreads, sizeof(Shared), s>>>(a, work, split.slices, split.per);
+        err = hipGetLastError();
+    }
+    return err;
+}
+
+template <typename T>
+hipError_t launch(const SampleArgs &a, void *workspace, hipStream_t s) {
+    // Measured (us, one workgroup a row | slices; bf16, unless said):
+    //   r x v                  no filter  top-p 0.95  min-p    top-k 50  greedy
+    //   1 x 65536              18 | 18    28 | 27     21 | 20  12 | 17   7 | 9
+    //   1 x 131072             27 | 18    40 | 30     31 | 20  14 | 18   10 | 9
+    //   8 x 131072             29 | 19    42 | 33     33 | 22  15 | 20   10 | 10
+    //   64 x 131072            30 | 31    43 | 44     33 | 31  15 | 20   11 | 12
+    //   1 x 1000000 fp32      180 | 24               188 | 28  43 | 22   74 | 11
+    const Split split = sample_split(a.r, a.v, sizeof(T));
+    const bool light = (a.set.top_ks == nullptr && a.set.top_k > 0) ||
+                       (a.set.temperatures == nullptr && !(a.set.temperature > 0.0f));
+    if (split.slices > 1 && (!light || a.v * int64_t(sizeof(T)) >= kSplitLight))
+        return launch_split<T>(a, split, workspace, s);
     static std::atomic<uint64_t> told{0};
     hipError_t err = allow_lds(reinterpret_cast<const void *>(row_kernel<T>), int(sizeof(Shared)), told);
     // a workgroup per row: a loop over rows in the kernel would keep what the
@@ -1121,6 +1443,8 @@ hipError_t launch(const SampleArgs &a, hipStream_t s) {
     }
     return err;
 }
+
+static_assert(sizeof(Slice) <= kSampleSlice, "the workspace holds the slices");
 
 }  // namespace
 }  // namespace rt
@@ -1141,9 +1465,9 @@ extern "C" rt_status rt_sample_rows(const void *logits, int32_t dtype, int64_t r
     hipStream_t s = static_cast<hipStream_t>(stream);
     hipError_t err;
     switch (dtype) {
-        case RT_DTYPE_FLOAT32: err = rt::launch<float>(a, s); break;
-        case RT_DTYPE_BFLOAT16: err = rt::launch<rt::bf16_t>(a, s); break;
-        default: err = rt::launch<rt::fp16_t>(a, s);
+        case RT_DTYPE_FLOAT32: err = rt::launch<float>(a, workspace, s); break;
+        case RT_DTYPE_BFLOAT16: err = rt::launch<rt::bf16_t>(a, workspace, s); break;
+        default: err = rt::launch<rt::fp16_t>(a, workspace, s);
     }
     if (err != hipSuccess) {
         (void)hipGetLastError();

@@ -131,7 +131,7 @@ rt_status rt_check_sample_rows(const void *logits, int32_t dtype, int64_t r, int
 
 int64_t rt_sample_rows_workspace(int64_t r, int64_t v) {
     if (r < 0 || r > kMaxN || v < 1 || v > kMaxN) return -1;
-    return 0;
+    return rt::sample_workspace(r, v);
 }
 
 }  // extern "C"
