@@ -141,7 +141,7 @@ struct Product {
     int64_t ldo;
     int64_t m, n;
     int k;
-    bool vec_out;  // 16 bytes of neighbouring outputs may be stored at once
+    bool aligned_out;  // every row of out starts at a multiple of 16 bytes
 
     __device__ __forceinline__ const int8_t *a_end() const { return a + (m - 1) * lda + k; }
     __device__ __forceinline__ const int8_t *b_end() const { return b + (n - 1) * ldb + k; }
@@ -189,11 +189,13 @@ __device__ __forceinline__ void store_row(const Product &p, int64_t i, int64_t j
         v[e] = static_cast<O>(y);
     }
     O *o = static_cast<O *>(p.out) + i * p.ldo + j;
-    if (p.vec_out && j + N <= p.n) {
-        if (NT)
+    if (j + N <= p.n) {
+        // gfx950 stores to unaligned addresses, too; past the caches only whole pieces of a line
+        typedef Piece Anywhere __attribute__((aligned(sizeof(O))));
+        if (NT && p.aligned_out)
             __builtin_nontemporal_store(v, reinterpret_cast<Piece *>(o));
         else
-            *reinterpret_cast<Piece *>(o) = v;
+            *reinterpret_cast<Anywhere *>(o) = v;
     } else {
 #pragma unroll
         for (int e = 0; e < N; ++e)
@@ -457,17 +459,8 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(Product p, int tiles
 #pragma unroll
     for (int s = 0; s < STAGES - 1; ++s)
         if (s < steps) stage(s, s);
-    int buf = 0;
-    for (int step = 0; step < steps; ++step) {
-        // this step's loads are the oldest of those in flight
-        if (step + STAGES - 2 < steps)
-            wait_vmcnt<(STAGES - 2) * (LA + LB)>();
-        else
-            wait_vmcnt<0>();
-        barrier();  // every wave's loads of this step have landed, its reads of the step before are done
-        if (step + STAGES - 1 < steps) stage(step + STAGES - 1, buf == 0 ? STAGES - 1 : buf - 1);
+    auto multiply = [&](int buf) {
         const int8_t *la = lds + buf * kBuf, *lb = la + BM * 128;
-        if (++buf == STAGES) buf = 0;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             i32x4 fa[FM], fb[FN];
@@ -486,22 +479,35 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(Product p, int tiles
 #pragma unroll
                 for (int h = 0; h < FM; ++h) acc[f][h] = mfma16(fb[f], fa[h], acc[f][h]);
         }
+    };
+    int buf = 0;
+    for (int step = 0; step < steps; ++step) {
+        // this step's loads are the oldest of those in flight
+        if (step + STAGES - 2 < steps)
+            wait_vmcnt<(STAGES - 2) * (LA + LB)>();
+        else
+            wait_vmcnt<0>();
+        barrier();  // every wave's loads of this step have landed, its reads of the step before are done
+        if (step + STAGES - 1 < steps) stage(step + STAGES - 1, buf == 0 ? STAGES - 1 : buf - 1);
+        multiply(buf);
+        if (++buf == STAGES) buf = 0;
     }
-    // the values after the last whole step, straight from global memory
-    for (int k0 = steps * 128; k0 < p.k; k0 += 64) {
-        const int valid = p.k - k0 - g * 16;
-        i32x4 fa[FM];
-#pragma unroll
-        for (int h = 0; h < FM; ++h)
-            fa[h] = load_part(p.a + min(i0 + wm * TM + h * 16 + r16, p.m - 1) * p.lda + k0 + g * 16, valid, p.a_end());
-#pragma unroll
-        for (int f = 0; f < FN; ++f) {
-            const i32x4 fb =
-                load_part(p.b + min(j0 + wn * TN + row_of<PAIRS>(f, r16), p.n - 1) * p.ldb + k0 + g * 16, valid,
-                          p.b_end());
-#pragma unroll
-            for (int h = 0; h < FM; ++h) acc[f][h] = mfma16(fb, fa[h], acc[f][h]);
-        }
+    // The values after the last whole step, zeros behind them, through registers
+    // into the next buffer: it was last read STAGES steps ago, ahead of a barrier.
+    if (steps * 128 < p.k) {
+        auto fill = [&](const int8_t *base, const int *offset, int count, const int8_t *end, int8_t *to, bool pairs) {
+            for (int i = 0; i < count; ++i) {
+                const int r = (i * NW + wave) * 8 + (lane >> 3);
+                const int unit = (lane & 7) ^ (pairs ? unit_swap<true>(r) : unit_swap<false>(r));
+                *reinterpret_cast<i32x4 *>(to + (i * NW + wave) * 1024 + lane * 16) =
+                    load_part(base + offset[i] + steps * 128, p.k - steps * 128 - unit * 16, end);
+            }
+        };
+        int8_t *to = lds + buf * kBuf;
+        fill(abase, av, LA, p.a_end(), to, false);
+        fill(bbase, bv, LB, p.b_end(), to + BM * 128, PAIRS);
+        barrier();
+        multiply(buf);
     }
     // 16 bytes a lane: 4 columns of fp32, 8 of a two-byte type
     constexpr int kSide = PAIRS ? 2 : 1;
@@ -550,7 +556,7 @@ bool aligned16(const void *ptr, int64_t ld) {
 
 template <typename O>
 hipError_t launch_product(Product p, hipStream_t s) {
-    p.vec_out = reinterpret_cast<uintptr_t>(p.out) % 16 == 0 && p.ldo % (16 / sizeof(O)) == 0;
+    p.aligned_out = reinterpret_cast<uintptr_t>(p.out) % 16 == 0 && p.ldo % (16 / sizeof(O)) == 0;
     auto tiles = [&](int64_t bm, int64_t bn) { return ((p.m + bm - 1) / bm) * ((p.n + bn - 1) / bn); };
     // a tile's row offsets are 32-bit: 255 ld + depth; and a grid has fewer than 2^32 threads
     const bool in_tiles = aligned16(p.a, p.lda) && aligned16(p.b, p.ldb) && p.lda <= (1 << 22) && p.ldb <= (1 << 22) &&
@@ -611,8 +617,7 @@ hipError_t launch_few_as(const void *x, int64_t ldx, const Product &p, int32_t o
     }
 }
 
-hipError_t launch_few_rows(const void *x, int32_t dtype, int64_t ldx, Product p, int32_t out_dtype, hipStream_t s) {
-    p.vec_out = reinterpret_cast<uintptr_t>(p.out) % 16 == 0 && p.ldo % (out_dtype == RT_DTYPE_FLOAT32 ? 4 : 8) == 0;
+hipError_t launch_few_rows(const void *x, int32_t dtype, int64_t ldx, const Product &p, int32_t out_dtype, hipStream_t s) {
     switch (dtype) {
         case RT_DTYPE_FLOAT32: return launch_few_as<float>(x, ldx, p, out_dtype, s);
         case RT_DTYPE_BFLOAT16: return launch_few_as<bf16_t>(x, ldx, p, out_dtype, s);

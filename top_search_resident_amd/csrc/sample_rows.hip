@@ -586,7 +586,7 @@ __device__ __forceinline__ void write_drawn(Output out, int64_t r, uint32_t toke
 }
 
 // find_first for at most two elements a thread (weight 0: none), `n` in all, with
-// keys in [least, most].  Once at most kSmall are left, eight threads compare
+// keys in [least, most] (most = 0: anywhere).  Once at most kSmall are left, eight threads compare
 // one of them with all.  Returns true to the one thread that holds the element
 // (the last one, where the weights do not reach the target; key 0, where there
 // are none).  Uses sh.list and sh.bin.
@@ -597,7 +597,7 @@ __device__ __forceinline__ bool find_in_pairs(Shared &sh, Pair p, uint32_t n, ui
                                               uint64_t target, uint64_t *found) {
     const int t = threadIdx.x, lane = t & 63;
     for (;;) {
-        if (n > kSmall) {
+        if (n > kSmall && most != 0) {
             __syncthreads();
             for (int i = t; i < kSearch; i += kThreads) sh.bin[i] = 0;
             __syncthreads();
@@ -663,38 +663,40 @@ __device__ __forceinline__ bool find_in_pairs(Shared &sh, Pair p, uint32_t n, ui
     }
 }
 
-// Sorts sh.list[0, n) down, zeros behind it to the next power of two from 128
-// on.  Pairs at distances up to 64 stay within one wave's 128 entries.
-__device__ __forceinline__ void sort_list(Shared &sh, uint32_t n) {
-    const uint32_t t = threadIdx.x;
-    uint32_t size = 128;
-    while (size < n) size *= 2;
-    for (uint32_t i = n + t; i < size; i += kThreads) sh.list[i] = 0;
-    __syncthreads();
-    for (uint32_t k = 2; k <= size; k *= 2) {
-        for (uint32_t j = k / 2; j > 0; j /= 2) {
-            if (t < size / 2) {
-                const uint32_t i = 2 * t - (t & (j - 1)), l = i + j;
-                const uint64_t a = sh.list[i], b = sh.list[l];
-                if ((a < b) == ((i & k) == 0)) sh.list[i] = b, sh.list[l] = a;
-            }
-            if (j > 64 || (j == 1 && k >= 128 && k < size)) {
-                __syncthreads();
-            } else {
-                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-                __builtin_amdgcn_wave_barrier();
-            }
-        }
+// sh.list[0, n), two elements a thread, with their weights.
+__device__ __forceinline__ Pair pairs_of_list(Shared &sh, uint32_t n, const Weights &weight) {
+    Pair p;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const uint32_t j = threadIdx.x + e * kThreads;
+        p.key[e] = j < n ? sh.list[j] : 0;
+        p.weight[e] = j < n ? weight(key_value(p.key[e])) : 0;
     }
+    return p;
+}
+
+// The key find_in_pairs finds, to all threads (0: no weight at all).
+__device__ __forceinline__ uint64_t find_key(Shared &sh, const Pair &p, uint32_t n, uint64_t least, uint64_t most,
+                                             uint64_t target) {
+    uint64_t key;
+    if (find_in_pairs(sh, p, n, least, most, target, &key)) sh.before = key;
     __syncthreads();
+    return sh.before;
+}
+
+__device__ __forceinline__ void keep_from(Pair &p, uint64_t key) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+        if (p.key[e] < key) p.weight[e] = 0;
 }
 
 // The rest of a row whose kept elements are all in sh.list[0, n): top-k and
 // top-p (where on), min-p and the draw.  A barrier has followed the list.
-// row_value(i) is logit i.
+// All its logits reach `from` (-inf: not known); row_value(i) is logit i of v.
 template <typename Value>
 __device__ __forceinline__ void draw_from_list(Shared &sh, Output out, int64_t r, uint32_t n, const Weights &weight,
-                                               const Settings &set, float least, uint32_t v, Value row_value) {
+                                               const Settings &set, float least, float from, uint32_t v,
+                                               Value row_value) {
     const uint32_t t = threadIdx.x;
     const uint32_t limit = set.top_k ? min(n, uint32_t(set.top_k)) : n;
     if (n <= kSmall) {
@@ -737,40 +739,29 @@ __device__ __forceinline__ void draw_from_list(Shared &sh, Output out, int64_t r
         if (mine && kept && run < aim && run + w >= aim) write_drawn(out, r, key_index(key), x, sum, weight);
         return;
     }
-    sort_list(sh, n);
-    const uint64_t k0 = sh.list[2 * t], k1 = sh.list[2 * t + 1];
-    const float x0 = key_value(k0), x1 = key_value(k1);
-    bool keep0 = 2 * t < limit, keep1 = 2 * t + 1 < limit;
-    const uint64_t w0 = keep0 ? weight(x0) : 0, w1 = keep1 ? weight(x1) : 0;
-    if (set.top_p < 1.0f) {
-        uint64_t z;
-        const uint64_t pre = block_scan(sh, w0 + w1, &z);
-        const uint64_t aim = at_least(set.top_p, z);
-        keep0 = keep0 && pre < aim;
-        keep1 = keep1 && pre + w0 < aim;
+    Pair p = pairs_of_list(sh, n, weight);
+    const uint64_t first_key = uint64_t(ordered(from)) << 32;
+    const uint64_t last_key = from > -INFINITY ? uint64_t(ordered(float(weight.top))) << 32 | 0xffffffffu : 0;
+    if (limit < n) {
+        const uint64_t k = find_key(sh, Pair{{p.key[0], p.key[1]}, {p.key[0] ? 1u : 0u, p.key[1] ? 1u : 0u}}, n,
+                                    first_key, last_key, limit);
+        keep_from(p, k);
     }
-    keep0 = keep0 && x0 >= least;
-    keep1 = keep1 && x1 >= least;
-    const uint64_t sum = block_add(sh, (keep0 ? w0 : 0) + (keep1 ? w1 : 0));
-    const uint64_t i0 = uint32_t(k0), i1 = uint32_t(k1);  // by index, the lowest first
+    if (set.top_p < 1.0f) {
+        const uint64_t z = block_add(sh, p.weight[0] + p.weight[1]);
+        keep_from(p, find_key(sh, p, n, first_key, last_key, at_least(set.top_p, z)));
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+        if (!(key_value(p.key[e]) >= least)) p.weight[e] = 0;
+    const uint64_t sum = block_add(sh, p.weight[0] + p.weight[1]);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) p.key[e] = uint32_t(p.key[e]);  // by index, the lowest first
     uint64_t key;
-    if (find_in_pairs(sh, Pair{{i0, i1}, {keep0 ? w0 : 0, keep1 ? w1 : 0}}, n, ~(v - 1), 0xffffffffu,
-                      above(set.u, sum), &key)) {
+    if (find_in_pairs(sh, p, n, ~(v - 1), 0xffffffffu, above(set.u, sum), &key)) {
         const uint32_t token = key_index(key);
         write_drawn(out, r, token, row_value(token), sum, weight);
     }
-}
-
-// sh.list[0, n), two elements a thread, with their weights.
-__device__ __forceinline__ Pair pairs_of_list(Shared &sh, uint32_t n, const Weights &weight) {
-    Pair p;
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        const uint32_t j = threadIdx.x + e * kThreads;
-        p.key[e] = j < n ? sh.list[j] : 0;
-        p.weight[e] = j < n ? weight(key_value(p.key[e])) : 0;
-    }
-    return p;
 }
 
 // The draw once the segments' kept weights are in sh.seg: the element of the
@@ -1004,12 +995,8 @@ __device__ __forceinline__ void settle_list(Shared &sh, const Row<T> &row, const
                                             const Border &border, float lo, float hi, float least, Cut &cut) {
     const Pair p = pairs_of_list(sh, n, weight);
     if (border.by_p) {
-        uint64_t key;
-        if (find_in_pairs(sh, p, n, uint64_t(ordered(lo)) << 32, (uint64_t(ordered(hi)) << 32) | 0xffffffffu,
-                          border.target - border.before, &key))
-            sh.before = key;
-        __syncthreads();
-        key = sh.before;
+        const uint64_t key = find_key(sh, p, n, uint64_t(ordered(lo)) << 32, (uint64_t(ordered(hi)) << 32) | 0xffffffffu,
+                                      border.target - border.before);
         if (key) cut.from_key(key);  // else the bin's weights all round to 0: what it holds cannot be drawn
     }
     cut.from_value(least);
@@ -1072,7 +1059,7 @@ __device__ __forceinline__ void sample_row(Shared &sh, const SampleArgs &args, i
     const auto value = [&](uint32_t i) { return static_cast<float>(row.p[i]); };
     if (row.v <= kList) {
         const uint32_t n = row.template collect<false>(sh, -__FLT_MAX__, INFINITY);
-        return draw_from_list(sh, out, r, n, weight, set, least, uint32_t(row.v), value);
+        return draw_from_list(sh, out, r, n, weight, set, least, -INFINITY, uint32_t(row.v), value);
     }
     Cut cut;
     if (set.top_k) {
@@ -1090,7 +1077,7 @@ __device__ __forceinline__ void sample_row(Shared &sh, const SampleArgs &args, i
                 // a wave takes about as long for one thread's place as for 64 threads' chunk
                 const uint32_t n = set.top_k <= 128 ? row.collect_from(sh, from, mine)
                                                     : row.template collect<false>(sh, from, INFINITY);
-                if (n <= kList) return draw_from_list(sh, out, r, n, weight, set, least, uint32_t(row.v), value);
+                if (n <= kList) return draw_from_list(sh, out, r, n, weight, set, least, from, uint32_t(row.v), value);
             }
         }
         cut.from_key(border_in_row<T>(sh, row, false, weight, -__FLT_MAX__, INFINITY, cut, uint64_t(set.top_k)));
@@ -1370,7 +1357,7 @@ __global__ __launch_bounds__(kThreads) void split_draw_kernel(SampleArgs args, S
     const Weights weight = weights_of(sh, args, top, set.temperature);
     const float least = set.least(top);
     if (set.top_k)
-        return draw_from_list(sh, out, r, n, weight, set, least, uint32_t(row.v),
+        return draw_from_list(sh, out, r, n, weight, set, least, -INFINITY, uint32_t(row.v),
                               [&](uint32_t i) { return static_cast<float>(row.p[i]); });
     Cut cut;
     const Border border = slice.own->border;
