@@ -69,6 +69,13 @@ def test_long_rows(dtype, v, r, f):
     check(x, u, **FILTERS[f])
 
 
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("f", range(len(FILTERS)))
+def test_many_rows(dtype, f):
+    x, u = logits(270, 6007, dtype, 500 + f)
+    check(x, u, **FILTERS[f])
+
+
 def test_long_rows_of_every_kind_at_once():
     """Shared rows (several workgroups each): empty, one token, greedy, infinite, tied, masked and flat rows
     with settings of their own, in one call; then each with no filter, top-p, min-p and top-k for all."""
@@ -94,7 +101,7 @@ def test_long_rows_of_every_kind_at_once():
 
 
 @pytest.mark.parametrize("dtype", list(TYPES))
-@pytest.mark.parametrize("r,v", [(40, 3001), (9, 200001), (3, 300000)])
+@pytest.mark.parametrize("r,v", [(40, 3001), (9, 200001), (3, 300000), (300, 700), (290, 20011)])
 def test_settings_of_each_row(dtype, r, v):
     x, u = logits(r, v, dtype, 77 + r)
     g = torch.Generator().manual_seed(8)
