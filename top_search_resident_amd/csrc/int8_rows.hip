@@ -364,11 +364,12 @@ hipError_t launch_few(const void *x, int64_t ldx, const Product &p, hipStream_t 
 }
 
 // 16 bytes per lane from base + voff to LDS lds + 16 lane (kept in the caches:
-// other workgroups read the same rows).
+// other workgroups read the same rows).  A load to LDS must not follow the
+// write of M0 at once: it needs one instruction between.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void dma16(const void *base, int voff, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(base), "s"(lds)
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(base), "s"(lds)
                  : "memory", "m0");
 }
 #pragma clang diagnostic pop
