@@ -159,6 +159,64 @@ def test_matmul_largest_sums(m, k):
     assert (host(y) == float(k * 2 ** 14)).all()
 
 
+@pytest.mark.parametrize("m,n,pitch", [(1100, 300, 1 << 22), (9, 20, 2 ** 31 - 1), (70, 33, (1 << 26) + 5)])
+def test_matmul_rows_far_apart(m, n, pitch):
+    """Row offsets past 32 bits, on both sides and in the output."""
+    g = torch.Generator().manual_seed(m)
+    k = 300
+    far = torch.empty(m, pitch, dtype=torch.int8, device="cuda")[:, :k]
+    far.copy_(int8_rows(m, k, g))
+    b, sa, sb = int8_rows(n, k, g, 304), scales(m, g), scales(n, g)
+    check(matmul_int8(far, sa, b, sb), host(far), host(sa), host(b), host(sb))
+    check(matmul_int8(b, sb, far, sa), host(b), host(sb), host(far), host(sa))
+    del far
+    a = int8_rows(m, k, g, 304)
+    out = torch.empty(m, pitch // 2, dtype=torch.bfloat16, device="cuda")[:, :n]
+    check(matmul_int8(a, sa, b, sb, out=out), host(a), host(sa), host(b), host(sb))
+
+
+def test_more_rows_than_a_launch_has_workgroups():
+    g = torch.Generator().manual_seed(5)
+    n = (1 << 24) + 37
+    b = torch.randint(-128, 128, (n, 1), dtype=torch.int8, generator=g).cuda()
+    a = torch.full((1, 1), -3, dtype=torch.int8, device="cuda")
+    one = torch.ones(n, device="cuda")
+    assert torch.equal(matmul_int8(a, one[:1], b, one)[0], b[:, 0].float() * -3)
+    x = torch.randint(-127, 128, ((1 << 20) + 5, 3), generator=g).float()
+    x[:, 1] = 127.0
+    q, s = quantize_rows_int8(x.cuda())
+    assert (s == 1).all() and torch.equal(q.cpu().float(), x)
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 512, 512), (20, 300, 800)])
+def test_streams_and_graphs_with_a_workspace_each(m, n, k):
+    """Two graphs of the same shapes, replayed at the same time on two streams."""
+    g = torch.Generator().manual_seed(6)
+    w, sw = int8_rows(n, k, g, (k + 15) // 16 * 16), scales(n, g) * 0.01
+    jobs = []
+    for _ in range(2):
+        x = torch.randn(m, k, generator=g).cuda()
+        ws = torch.empty(max(1, linear_int8_workspace(m, n, k)), dtype=torch.uint8, device="cuda")
+        out = torch.empty(m, n, device="cuda")
+        linear_int8(x, w, sw, out=out, workspace=ws)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            linear_int8(x, w, sw, out=out, workspace=ws)
+        jobs.append((x, out, graph, torch.cuda.Stream()))
+    for seed in range(4):
+        for x, out, _, _ in jobs:
+            x.copy_(torch.randn(m, k, generator=g))
+            out.fill_(-1.0)
+        torch.cuda.synchronize()
+        for _, _, graph, stream in jobs:
+            with torch.cuda.stream(stream):
+                graph.replay()
+        torch.cuda.synchronize()
+        for x, out, _, _ in jobs:
+            assert torch.equal(out, linear_int8(x, w, sw))
+
+
 @pytest.mark.parametrize("dtype", list(TYPES))
 @pytest.mark.parametrize("m,n,k", [(1, 77, 100), (1, 1024, 1024), (1, 8, 8192), (1, 300, 8193), (1, 8193, 64),
                                    (3, 500, 768), (4, 33, 2048), (4, 96, 4096), (5, 96, 1000), (31, 200, 777),
