@@ -184,6 +184,62 @@ def test_extreme_settings(s):
     check(x, u, exact_ties=True, **s)
 
 
+@pytest.mark.parametrize("r,v,first", [(24, 100001, 0), (24, 100001, 33000), (300, 20001, 10240), (2, 270000, 8200),
+                                       (2, 270000, 0)])
+def test_random_number_one_behind_the_rounded_sums(r, v, first):
+    """The finite logits lie at the start of one of the parts whose weights are summed on their own,
+    with nothing behind them there: the sums' last unit still draws the last of them."""
+    g = torch.Generator().manual_seed(v + first)
+    x = torch.full((r, v), -INF)
+    x[:, first + 10:first + 900] = torch.randn(r, 890, generator=g) * 2
+    for s in (dict(), dict(temperature=1.3), dict(top_p=0.9999), dict(min_p=1e-6)):
+        for u in (1.0, 3.0, 1.0 - 2.0 ** -24):
+            out = torch.full((r,), -7, dtype=torch.int32, device="cuda")
+            sample_rows(x.cuda(), torch.full((r,), u).cuda(), out_token=out, **s)
+            assert (out >= first + 10).all() and (out < first + 900).all()
+            if u >= 1:
+                check(x, torch.full((r,), u), exact_ties=True, **s)
+
+
+@pytest.mark.parametrize("r", [2, 20])
+def test_weights_that_only_together_make_a_unit(r):
+    """Ten tokens of three tenths of the smallest unit each: their part of the row weighs 3 units, none of
+    them alone one."""
+    v = 140000  # units of 2^-44 of the largest weight
+    x = torch.full((r, v), -INF)
+    x[:, 5] = 0.0
+    x[:, 131500:131510] = float(np.log(0.3 * 2.0 ** -44))
+    check(x, torch.ones(r), exact_ties=True)
+
+
+def test_longest_row():
+    """2^31 - 1 logits, by many workgroups and (infinite ones) by one."""
+    v = 2 ** 31 - 1
+    x = torch.full((1, v), -INF, dtype=torch.bfloat16, device="cuda")
+    places = [5, 70001, 2 ** 30 + 3, v - 9, v - 1]
+    values = torch.tensor([1.0, 3.0, 2.0, 0.0, 2.5]).to(torch.bfloat16)
+    x[0, places] = values.cuda()
+    for u in (0.0, 0.3, 0.9, 1.0):
+        for s in (dict(), dict(top_k=3), dict(top_p=0.6), dict(min_p=0.3), dict(temperature=0.0)):
+            token, prob = sample_rows(x, torch.tensor([u]).cuda(), **s)
+            e, p, margin, _ = row_oracle.draw(values.double().numpy(), u, **s)
+            assert margin > 1e-6  # 5 weights, each off by half of 2^-31 at most
+            assert token.item() == places[e] and abs(prob.item() - p) <= p * 1e-6
+    x[0, places[1:4]] = INF
+    assert sample_rows(x, torch.tensor([0.5]).cuda())[0].item() == places[2]
+
+
+def test_rows_far_apart_and_more_rows_than_a_launch():
+    far = torch.empty(3, 2 ** 31 - 1, dtype=torch.bfloat16, device="cuda")[:, :700]
+    x, u = logits(3, 700, "bf16", 43)
+    far.copy_(x)
+    check(far, u, top_k=40, top_p=0.9)
+    r = (1 << 20) + 3
+    x = torch.randn(r, 3, generator=torch.Generator().manual_seed(44)).cuda()
+    token, prob = sample_rows(x, torch.zeros(r, device="cuda"), temperature=0.0)
+    assert torch.equal(token.long(), x.argmax(1)) and (prob == 1).all()
+
+
 def test_random_numbers_at_the_ends():
     x, _ = logits(6, 700, "fp32", 13)
     x[:, :5] = -INF

@@ -812,12 +812,11 @@ __device__ __forceinline__ void draw_from_row(Shared &sh, Output out, int64_t r,
         }
         uint64_t all;
         uint64_t run = block_scan(sh, mine, &all);
-        if (all >= target || c + 1 == end) {
-            const uint64_t aim = min(target, all);
-            if (run < aim && run + mine >= aim) {
+        if (all >= target) {
+            if (run < target && run + mine >= target) {
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
-                    if (run < aim && run + w[e] >= aim)
+                    if (run < target && run + w[e] >= target)
                         write_drawn(out, r, i + e, element<T>(x, e), sum, weight);
                     run += w[e];
                 }
@@ -825,6 +824,29 @@ __device__ __forceinline__ void draw_from_row(Shared &sh, Output out, int64_t r,
             return;
         }
         target -= all;
+    }
+    // A segment's sum is its bins', each rounded as one, and can be some units above
+    // the sum of its elements': a target up there goes to the last element that
+    // weighs a unit, or, where they do so only together, to the last of them.
+    uint64_t behind = 0;
+    row.each(
+        [&](float y, uint32_t i) {
+            double f;
+            if (cut(y, i) && weight.split(y, &f) > 1 - kMass) {
+                const uint64_t key = (uint64_t(weight(y) != 0) << 32) | i;
+                behind = key > behind ? key : behind;
+            }
+        },
+        seg * row.per, end);
+    behind = wave_max64(behind);
+    __syncthreads();
+    if (threadIdx.x == 0) sh.hi = 0;
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) atomicMax(reinterpret_cast<ull *>(&sh.hi), ull(behind));
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        const uint32_t i = uint32_t(sh.hi);
+        write_drawn(out, r, i, static_cast<float>(row.p[i]), sum, weight);
     }
 }
 
