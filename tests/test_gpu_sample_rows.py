@@ -184,6 +184,14 @@ def test_extreme_settings(s):
     check(x, u, exact_ties=True, **s)
 
 
+@pytest.mark.parametrize("r,v", [(4, 900), (30, 9000), (2, 270000), (300, 5000)])
+@pytest.mark.parametrize("s", [dict(), dict(min_p=1.0), dict(min_p=0.5), dict(top_p=0.5), dict(top_k=600, min_p=1.0)])
+def test_infinite_temperature_weighs_all_the_same(r, v, s):
+    x, u = logits(r, v, "fp32", 41)
+    x[:, 1::3] = -INF
+    check(x, u, exact_ties=True, temperature=INF, **s)
+
+
 @pytest.mark.parametrize("r,v,first", [(24, 100001, 0), (24, 100001, 33000), (300, 20001, 10240), (2, 270000, 8200),
                                        (2, 270000, 0)])
 def test_random_number_one_behind_the_rounded_sums(r, v, first):

@@ -564,9 +564,10 @@ struct Settings {
         single = !(temperature > 0.0f) || top_k == 1 || !(top_p > 0.0f) || !(min_p <= 1.0f);
         if (top_k < 0 || top_k >= a.v) top_k = 0;
     }
-    // min-p as a logit: the smallest fp32 at or above top + T ln(min_p)
+    // min-p as a logit: the smallest fp32 at or above top + T ln(min_p); at an
+    // infinite T all weigh the same
     __device__ __forceinline__ float least(float top) const {
-        if (!(min_p > 0.0f)) return -INFINITY;
+        if (!(min_p > 0.0f) || temperature == INFINITY) return -INFINITY;
         const float x = __double2float_ru(double(top) + double(temperature) * log(double(min_p)));
         return x <= top ? x : top;
     }
