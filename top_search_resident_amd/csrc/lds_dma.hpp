@@ -16,8 +16,9 @@
 // waiting until at most N remain outstanding means every load issued before
 // the last N has landed.  Any VMEM instruction the compiler issues in between
 // only adds to the operations after a given load, so such a wait stays
-// correct (just more conservative).  M0 is set inside the same asm statement;
-// the kernels using this issue no other instruction that reads M0.
+// correct (just more conservative).  M0 is set inside the same asm statement,
+// with one instruction between (a load to LDS must not follow a write of M0 at
+// once); the kernels using this issue no other instruction that reads M0.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -30,12 +31,12 @@ namespace rt {
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void dma16_nt(const void *sbase, int voff, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1 nt" ::"v"(voff), "s"(sbase), "s"(lds)
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1 nt" ::"v"(voff), "s"(sbase), "s"(lds)
                  : "memory", "m0");
 }
 // 16 bytes per lane from the lane's own 64-bit address into LDS at lds + 16 * lane.
 __device__ __forceinline__ void dma16_nt_addr(const void *addr, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off nt" ::"v"(addr), "s"(lds) : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off nt" ::"v"(addr), "s"(lds) : "memory", "m0");
 }
 #pragma clang diagnostic pop
 
