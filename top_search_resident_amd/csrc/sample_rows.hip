@@ -69,11 +69,10 @@ __global__ __launch_bounds__(kThreads) void split_top_kernel(SampleArgs args, Sl
     const int t = threadIdx.x;
     SliceOf<T> slice(args, work, blockIdx.y, blockIdx.x, slices, per);
     const Settings set(args, blockIdx.y);
-    float own = -INFINITY;
-    slice.row.each_chunk([&](u32x4 x, int) {
-        const float m = Row<T>::largest(x);
-        own = m > own ? m : own;
-    });
+    Largest<T> largest;
+    slice.row.each_of_many([&](u32x4 x, int) { largest.add(x); }, slice.row.begin, slice.row.end);
+    float own = largest.value();
+    if (largest.nan()) own = slice.row.largest();
     slice.own->own[t] = own;
     float top = wave_max(own), floor = wave_min(own > -INFINITY ? own : INFINITY);
     if ((t & 63) == 0) sh.f[t >> 6] = top, sh.g[t >> 6] = floor;
@@ -129,7 +128,7 @@ __global__ __launch_bounds__(kThreads) void split_candidates_kernel(SampleArgs a
             from = count_edge(sh, set.top_k, top, floor, scale);
         }
         uint32_t n = kList + 1;
-        if (from > -INFINITY) n = slice.row.template collect<false>(sh, from, INFINITY);
+        if (from > -INFINITY) n = slice.row.collect(sh, from, top);
         return write_list(sh, slice.own, n);
     }
     const Weights weight = weights_of(sh, args, top, set.temperature);  // no factor is read
@@ -167,7 +166,7 @@ __global__ __launch_bounds__(kThreads) void split_border_kernel(SampleArgs args,
         find_edges(sh, weight, top, border.bin);
         __syncthreads();
         const float lo = sh.edge[0], hi = sh.edge[1];
-        write_list(sh, slice.own, slice.row.template collect<true>(sh, lo, hi));
+        write_list(sh, slice.own, slice.row.collect(sh, lo, fminf(next_below(hi), top)));
         if (t == 0) slice.own->lo = lo, slice.own->hi = fminf(hi, top);
     }
     if (t == 0) {

@@ -47,6 +47,7 @@ constexpr int kSearch = 2048; // bins of a search
 constexpr int kOwn = kSearch / kThreads;   // bins and list elements a thread
 constexpr int kTeam = kThreads / kSmall;   // threads that compare one of a small list
 constexpr int32_t kMostK = kList / 2;      // top-k up to here is looked for by list
+constexpr int kAtOnce = 4;    // chunks on their way in passes that do little
 constexpr int kPlaces = 4096; // 16-byte places that hold candidates
 
 // ------------------------------------------------------------------- weights
@@ -150,7 +151,10 @@ __device__ __forceinline__ uint32_t ordered(float x) {
 __device__ __forceinline__ float unordered(uint32_t o) {
     return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
 }
-__device__ __forceinline__ float next_below(float x) { return unordered(ordered(x) - 1); }
+__device__ __forceinline__ float next_below(float x) {
+    const uint32_t o = ordered(x) - 1;
+    return unordered(o == 0x7fffffffu ? o - 1 : o);  // below 0.0 is not -0.0
+}
 
 // Order of the elements as one 64-bit number, larger first: the logit, then the
 // index from the top down.
@@ -254,6 +258,19 @@ __device__ __forceinline__ uint64_t wave_scan(uint64_t v) {
     v = row_scan(v);
     v += dpp64<0x142, 0xa>(v);
     v += dpp64<0x143, 0xc>(v);
+    return v;
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp_u32(uint32_t v) {
+    return __builtin_amdgcn_update_dpp(0, int(v), CTRL, ROWS, 0xf, false);
+}
+__device__ __forceinline__ uint32_t wave_scan32(uint32_t v) {
+    v += dpp_u32<0x111, 0xf>(v);
+    v += dpp_u32<0x112, 0xf>(v);
+    v += dpp_u32<0x114, 0xf>(v);
+    v += dpp_u32<0x118, 0xf>(v);
+    v += dpp_u32<0x142, 0xa>(v);
+    v += dpp_u32<0x143, 0xc>(v);
     return v;
 }
 __device__ __forceinline__ uint64_t wave_add(uint64_t v) { return lane64(wave_scan(v), 63); }
@@ -378,12 +395,99 @@ __device__ __forceinline__ uint64_t find_first(Shared &sh, Each each, uint64_t t
 
 // ------------------------------------------------------------------- the row
 
-// Chunk c of thread t holds elements (c * 1024 + t) * E .. of the row; elements
+// A type's codes as whole numbers, several to a register: nonnegative values order
+// as their codes, negative ones the other way round.
+template <typename T>
+struct CodesOf {
+    typedef uint16_t U __attribute__((ext_vector_type(2)));
+    typedef int16_t S __attribute__((ext_vector_type(2)));
+    static constexpr uint32_t kSign = 0x8000u, kInf = __is_same(T, bf16_t) ? 0x7f80u : 0x7c00u;
+    static __device__ __forceinline__ uint32_t most(S v) { return uint32_t(uint16_t(v[0] > v[1] ? v[0] : v[1])); }
+    static __device__ __forceinline__ uint32_t least(U v) { return v[0] < v[1] ? v[0] : v[1]; }
+    static __device__ __forceinline__ float value(uint32_t code) {
+        return static_cast<float>(__builtin_bit_cast(T, uint16_t(code)));
+    }
+    static __device__ __forceinline__ uint32_t down(float x) {  // of the largest value up to x >= 0
+        if constexpr (__is_same(T, bf16_t)) return __float_as_uint(x) >> 16;
+        const uint32_t c = __builtin_bit_cast(uint16_t, static_cast<T>(x));
+        return value(c) > x ? c - 1 : c;
+    }
+};
+template <>
+struct CodesOf<float> {
+    typedef uint32_t U;
+    typedef int32_t S;
+    static constexpr uint32_t kSign = 0x80000000u, kInf = 0x7f800000u;
+    static __device__ __forceinline__ uint32_t most(S v) { return uint32_t(v); }
+    static __device__ __forceinline__ uint32_t least(U v) { return v; }
+    static __device__ __forceinline__ float value(uint32_t code) { return __uint_as_float(code); }
+    static __device__ __forceinline__ uint32_t down(float x) { return __float_as_uint(x); }
+};
+
+// The largest of many 16 bytes: of the nonnegative ones the largest signed code,
+// and where there are none the smallest unsigned one.  Two packed instructions
+// for two 2-byte logits, where unpacking, comparing and selecting take six.  A
+// positive NaN hides what is below it: nan() says so.
+template <typename T>
+struct Largest {
+    typedef CodesOf<T> C;
+    typename C::S most = typename C::S(0) + typename C::S(sizeof(T) == 2 ? -32768 : int32_t(0x80000000u));
+    typename C::U least = ~typename C::U(0);
+
+    __device__ __forceinline__ void add(u32x4 x) {
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            most = __builtin_elementwise_max(most, __builtin_bit_cast(typename C::S, uint32_t(x[d])));
+            least = __builtin_elementwise_min(least, __builtin_bit_cast(typename C::U, uint32_t(x[d])));
+        }
+    }
+    __device__ __forceinline__ bool nan() const {
+        const uint32_t m = C::most(most);
+        return m < C::kSign && m > C::kInf;
+    }
+    __device__ __forceinline__ float value() const {
+        const uint32_t m = C::most(most), n = C::least(least);
+        return m < C::kSign ? C::value(m) : (n <= (C::kSign | C::kInf) ? C::value(n) : -INFINITY);
+    }
+};
+
+// The logits in [lo, last], both of one sign, as a run of codes.
+template <typename T>
+struct Codes {
+    typedef CodesOf<T> C;
+    typename C::U first;
+    uint32_t width;
+    bool usable, empty;  // empty: the type has no value there
+
+    __device__ __forceinline__ Codes(float lo, float last) {
+        const bool negative = last < 0.0f;
+        const float small = negative ? -last : lo, large = negative ? -lo : last;  // magnitudes
+        const uint32_t below = C::down(small), to = C::down(large);
+        const uint32_t from = C::value(below) < small ? below + 1 : below;
+        usable = small > 0.0f;
+        empty = usable && from > to;
+        width = to - from;
+        first = typename C::U(0) + typename C::U(from | (negative ? C::kSign : 0u));
+    }
+    __device__ __forceinline__ bool any(u32x4 x) const {
+        typename C::U m = ~typename C::U(0);
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            const typename C::U off = __builtin_bit_cast(typename C::U, uint32_t(x[d])) - first;
+            m = __builtin_elementwise_min(m, off);
+        }
+        return C::least(m) <= width;
+    }
+};
+
+// Chunk c of thread t holds elements (c * kThreads + t) * E .. of the row; elements
 // past its end read as -inf.
 template <typename T>
 struct Row {
     static constexpr int E = 16 / sizeof(T);
     static constexpr int64_t kChunk = int64_t(kThreads) * E;
+    static constexpr uint32_t none =  // -inf
+        sizeof(T) == 4 ? 0xff800000u : (__is_same(T, bf16_t) ? 0xff80ff80u : 0xfc00fc00u);
     const T *p;
     int64_t v;
     int begin, end, per;  // the chunks that the passes below go over, and how many make a segment
@@ -404,7 +508,6 @@ struct Row {
     // row, moved down, -inf behind them.
     __device__ __forceinline__ u32x4 load_last(int64_t c, uint32_t t = threadIdx.x) const {
         const int64_t i = c * kChunk + int64_t(t) * E;
-        constexpr uint32_t none = sizeof(T) == 4 ? 0xff800000u : (__is_same(T, bf16_t) ? 0xff80ff80u : 0xfc00fc00u);
         u32x4 x = {none, none, none, none};
         if (i + E <= v) return load16(p + i);
         if (i >= v) return x;
@@ -455,6 +558,26 @@ struct Row {
 #pragma unroll 1
         for (; c < end; ++c) f(load(c), c);
     }
+    // The same for chunks c .. c1 - 1 with kAtOnce on their way at once, for passes that
+    // do little with them; behind the last, -inf once more.
+    template <typename F>
+    __device__ __forceinline__ void each_of_many(F f, int c, int c1) const {
+        const int whole = min(c1, int(v / kChunk));
+        u32x4 part = {none, none, none, none};
+        if (whole < c1) part = load_last(whole);
+#pragma unroll 1
+        for (; c < whole; c += kAtOnce) {
+            u32x4 x[kAtOnce];
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) x[i] = load_whole(min(c + i, whole - 1));
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+                const bool in = c + i < whole;
+                f(u32x4{in ? x[i][0] : none, in ? x[i][1] : none, in ? x[i][2] : none, in ? x[i][3] : none}, c + i);
+            }
+        }
+        if (whole < c1) f(part, whole);
+    }
     // f(value, index) of each element of chunks c .. c1 - 1, one chunk at a time: for
     // the rarely taken paths, where small code matters more
     template <typename F>
@@ -471,58 +594,80 @@ struct Row {
     __device__ __forceinline__ void each(F f) const {
         each(f, begin, end);
     }
-    static __device__ __forceinline__ float largest(u32x4 x) {  // -inf for NaN
+    __device__ __forceinline__ float largest() const {  // of this thread's elements, NaN passed over
         float m = -INFINITY;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const float y = element<T>(x, e);
-            m = y > m ? y : m;
-        }
+        each([&](float y, uint32_t) { m = y > m ? y : m; });
         return m;
     }
-    // The keys of the 16 bytes' elements from `lo` on and below `hi` (+inf: no end; no
-    // logit is infinite here) to sh.list, up to kList of them; sh.count counts them all.
-    static __device__ __forceinline__ void take(Shared &sh, u32x4 x, uint32_t i, float lo, float hi) {
+    // The keys of the 16 bytes' elements in [lo, last] (no logit is infinite here) to
+    // sh.list, up to kList of them; sh.count counts them all.
+    static __device__ __forceinline__ void take(Shared &sh, u32x4 x, uint32_t i, float lo, float last) {
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             const float y = element<T>(x, e);
-            if (y >= lo && y < hi) {
+            if (y >= lo && y <= last) {
                 const uint32_t at = atomicAdd(&sh.count, 1u);
                 if (at < kList) sh.list[at] = order_key(y, i + e);
             }
         }
     }
     // The whole row's; returns sh.count.  First the places of the 16 bytes that hold
-    // any (one note for a wave's, where noting each element would cost more than
-    // reading those again), then their elements, a thread each.  `END`: hi counts.
-    template <bool END>
-    __device__ __forceinline__ uint32_t collect(Shared &sh, float lo, float hi) const {
+    // any (a thread's as bits, noted together), then their elements, a thread each.
+    __device__ __forceinline__ uint32_t collect(Shared &sh, float lo, float last) const {
+        const Codes<T> codes(lo, last);
+        if (codes.empty) return 0;
         uint32_t *places = reinterpret_cast<uint32_t *>(sh.bin);
         __syncthreads();  // sh.bin, sh.found and sh.count have been read
         if (threadIdx.x == 0) sh.count = 0, sh.found = 0;
         __syncthreads();
-        each_chunk(
-            [&](u32x4 x, int c) {
-                bool any = false;
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const float y = element<T>(x, e);
-                    any |= END ? (y >= lo) & (y < hi) : y >= lo;
-                }
-                if (any) {
-                    const uint32_t at = atomicAdd(&sh.found, 1u);
-                    if (at < kPlaces) places[at] = uint32_t(c) * kThreads + threadIdx.x;
-                }
-            });
+        for (int c0 = begin; c0 < end; c0 += 32) {
+            const int c1 = min(c0 + 32, end);
+            uint32_t hit = 0;  // a bit for each of this thread's next 32 places
+            if (codes.usable) {
+                each_of_many([&](u32x4 x, int c) { hit |= codes.any(x) ? 1u << (c - c0) : 0u; }, c0, c1);
+            } else {
+                each([&](float y, uint32_t i) { hit |= y >= lo && y <= last ? 1u << (int(i / kChunk) - c0) : 0u; }, c0, c1);
+            }
+            if (__any(hit != 0)) {
+                uint32_t at = places_for(sh.found, __popc(hit));
+                for (; hit != 0 && at < kPlaces; hit &= hit - 1, ++at)
+                    places[at] = uint32_t(c0 + __builtin_ctz(hit)) * kThreads + threadIdx.x;
+            }
+        }
         __syncthreads();
         const uint32_t n = sh.found;
         if (n > kPlaces) return kList + 1;
-        for (uint32_t j = threadIdx.x; j < n; j += kThreads) {
-            const uint32_t c = places[j] / kThreads, t = places[j] % kThreads;
-            take(sh, load(c, t), index(c, t), lo, END ? hi : INFINITY);
+        for (uint32_t j0 = 0; j0 < n; j0 += kThreads) {
+            const uint32_t j = j0 + threadIdx.x;
+            u32x4 x = {none, none, none, none};
+            uint32_t i = 0, hit = 0;
+            if (j < n) {
+                const uint32_t c = places[j] / kThreads, t = places[j] % kThreads;
+                x = load(c, t);
+                i = index(c, t);
+            }
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const float y = element<T>(x, e);
+                hit |= (y >= lo) & (y <= last) ? 1u << e : 0u;
+            }
+            if (!__any(hit != 0)) continue;
+            uint32_t at = places_for(sh.count, __popc(hit));
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                if ((hit >> e & 1u) && at < kList) sh.list[at] = order_key(element<T>(x, e), i + e);
+                at += hit >> e & 1u;
+            }
         }
         __syncthreads();
         return sh.count;
+    }
+    // The first of `own` places after `count`, which it moves on by the wave's.
+    static __device__ __forceinline__ uint32_t places_for(uint32_t &count, uint32_t own) {
+        const uint32_t upto = wave_scan32(own);
+        uint32_t at = 0;
+        if ((threadIdx.x & 63) == 63) at = atomicAdd(&count, upto);
+        return __builtin_amdgcn_readlane(int(at), 63) + upto - own;
     }
     // The same without an end, where few threads' largest logit `own` reaches lo:
     // the waves take those threads' places one by one, a chunk a lane.
@@ -589,6 +734,19 @@ __device__ __forceinline__ void write_drawn(Output out, int64_t r, uint32_t toke
     int bin;
     const double w = weight.power(x, &bin);
     write_row(out, r, token, float(w * weight.zero[bin] / double(sum)));  // not rounded to whole units
+}
+
+// f(j) for j = g, g + kTeam, ... below n; what f reads of four at a time is on its way together.
+template <typename F>
+__device__ __forceinline__ void each_of_small(uint32_t n, uint32_t g, F f) {
+    uint32_t j = g;
+#pragma unroll 1
+    for (; j + 3 * kTeam < n; j += 4 * kTeam) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f(j + e * kTeam);
+    }
+#pragma unroll 1
+    for (; j < n; j += kTeam) f(j);
 }
 
 // find_first for at most kOwn elements a thread (weight 0: none), `n` in all, with
@@ -667,8 +825,10 @@ __device__ __forceinline__ bool find_in_shares(Shared &sh, Share p, uint32_t n, 
             if (i >= n) return false;
             const uint64_t key = sh.list[i], w = sh.weight[i];
             uint64_t run = 0;
-            for (uint32_t j = g; j < n; j += kTeam)
-                if (sh.list[j] > key) run += sh.weight[j];
+            for (uint32_t j = g; j < n; j += kTeam) {
+                const uint64_t other = sh.list[j], one = sh.weight[j];
+                run += other > key ? one : 0;
+            }
 #pragma unroll
             for (int o = 1; o < kTeam; o <<= 1) run += shfl_xor64(run, o);
             *found = key;
@@ -732,11 +892,12 @@ __device__ __forceinline__ void draw_from_list(Shared &sh, Output out, int64_t r
         __syncthreads();
         uint32_t rank = 0;
         uint64_t pre = 0;
-        for (uint32_t j = g; j < n; j += kTeam)
-            if (sh.list[j] > key) {
-                ++rank;
-                pre += sh.weight[j];
-            }
+        each_of_small(n, g, [&](uint32_t j) {
+            const bool ahead = sh.list[j] > key;
+            const uint64_t one = sh.weight[j];
+            rank += ahead ? 1 : 0;
+            pre += ahead ? one : 0;
+        });
 #pragma unroll
         for (int o = 1; o < kTeam; o <<= 1) {
             rank += uint32_t(__shfl_xor(int(rank), o));
@@ -753,8 +914,10 @@ __device__ __forceinline__ void draw_from_list(Shared &sh, Output out, int64_t r
         __syncthreads();
         const uint64_t sum = sh.hi, aim = above(set.u, sum);
         uint64_t run = 0;
-        for (uint32_t j = g; j < n; j += kTeam)
-            if (key_index(sh.list[j]) < key_index(key)) run += sh.weight[j];
+        each_of_small(n, g, [&](uint32_t j) {
+            const uint64_t other = sh.list[j], one = sh.weight[j];
+            run += key_index(other) < key_index(key) ? one : 0;
+        });
 #pragma unroll
         for (int o = 1; o < kTeam; o <<= 1) run += shfl_xor64(run, o);
         if (mine && kept && run < aim && run + w >= aim) write_drawn(out, r, key_index(key), x, sum, weight);
@@ -791,15 +954,15 @@ __device__ __forceinline__ void draw_from_list(Shared &sh, Output out, int64_t r
 template <typename T>
 __device__ __forceinline__ void draw_from_row(Shared &sh, Output out, int64_t r, const Row<T> &row,
                                               const Weights &weight, float u, const Cut &cut) {
-    uint64_t sum = 0;
-    int seg = 0, last = 0;
-    for (int s = 0; s < kSlices; ++s) {
-        sum += sh.seg[s];
-        if (sh.seg[s]) last = s;
-    }
+    // a lane for each segment
+    const int lane = threadIdx.x & 63;
+    const uint64_t own = lane < kSlices ? sh.seg[lane] : 0;
+    const uint64_t upto = wave_scan(own), sum = lane64(upto, 63);
     uint64_t target = above(u, sum);
-    while (seg < last && sh.seg[seg] < target) target -= sh.seg[seg++];
+    const int seg = __builtin_ctzll(__ballot(upto >= target));
+    target -= lane64(upto - own, seg);
     const int end = min((seg + 1) * row.per, row.end);
+#pragma unroll 1
     for (int c = seg * row.per; c < end; ++c) {
         const u32x4 x = row.load(c);
         const uint32_t i = row.index(c);
@@ -973,9 +1136,10 @@ __device__ __forceinline__ Weights weights_of(Shared &sh, const SampleArgs &args
 
 // The factors' table; a barrier follows before its first use.
 __device__ __forceinline__ void fill_factors(Shared &sh, int shift) {
+    // a thread's bins are kThreads apart, whole octaves: one power for all of them
+    const double part = exp2(double(threadIdx.x % kPerOctave) / -kPerOctave);
     for (int b = threadIdx.x; b < kMass; b += kThreads)
-        sh.factor[kMass - 1 - b] =
-            b < kMass - 1 ? __builtin_ldexp(exp2(double(b % kPerOctave) / -kPerOctave), shift - b / kPerOctave) : 0.0;
+        sh.factor[kMass - 1 - b] = b < kMass - 1 ? __builtin_ldexp(part, shift - b / kPerOctave) : 0.0;
 }
 
 // Counts x, at least floor, in the bins of [floor, top].
@@ -1063,14 +1227,22 @@ __device__ __forceinline__ void sample_row(Shared &sh, const SampleArgs &args, i
 
     // the largest logit, and the smallest finite one
     // of the threads' largest, each over every fourth of its chunks
-    float own[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-    row.each_chunk(
+    Largest<T> largest[4];
+    row.each_of_many(
         [&](u32x4 x, int c) {
-            const float m = Row<T>::largest(x);
 #pragma unroll
             for (int g = 0; g < 4; ++g)
-                if ((c & 3) == g) own[g] = m > own[g] ? m : own[g];
-        });
+                if ((c & 3) == g) largest[g].add(x);
+        },
+        0, row.end);
+    float own[4];
+    bool again = false;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) own[g] = largest[g].value(), again |= largest[g].nan();
+    if (again) {
+        own[0] = row.largest();
+        own[1] = own[2] = own[3] = -INFINITY;
+    }
     const float mine = fmaxf(fmaxf(own[0], own[1]), fmaxf(own[2], own[3]));
     float top = mine, floor = INFINITY;
 #pragma unroll
@@ -1103,30 +1275,29 @@ __device__ __forceinline__ void sample_row(Shared &sh, const SampleArgs &args, i
 
     const Weights weight = weights_of(sh, args, top, set.temperature);
     const float least = set.least(top);
-    const auto value = [&](uint32_t i) { return static_cast<float>(row.p[i]); };
-    if (row.v <= kList) {
-        const uint32_t n = row.template collect<false>(sh, -__FLT_MAX__, INFINITY);
-        return draw_from_list(sh, out, r, n, weight, set, least, -INFINITY, uint32_t(row.v), value);
+    // rows that fit the list, and top-k's elements where a list of few more holds them
+    float from = row.v <= kList ? -__FLT_MAX__ : -INFINITY;
+    if (row.v > kList && set.top_k && set.top_k <= kMostK && floor < top) {
+        // A value that at least k elements reach, and few more: the lower edge of the
+        // bin where the count of those 4 kThreads largest logits reaches k (of so many,
+        // one seldom hides another of the first k).
+        const float scale = count_scale(top, floor);
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+            if (own[g] > -INFINITY) count_logit(sh, own[g], top, scale);
+        __syncthreads();
+        from = count_edge(sh, set.top_k, top, floor, scale);
+    }
+    if (from > -INFINITY) {
+        // a wave takes about as long for one thread's place as for 64 threads' chunk
+        const bool few = row.v > kList && set.top_k <= 128;
+        const uint32_t n = few ? row.collect_from(sh, from, mine) : row.collect(sh, from, top);
+        if (n <= kList)
+            return draw_from_list(sh, out, r, n, weight, set, least, row.v > kList ? from : -INFINITY, uint32_t(row.v),
+                                  [&](uint32_t i) { return static_cast<float>(row.p[i]); });
     }
     Cut cut;
     if (set.top_k) {
-        // A value that at least k elements reach, and few more: the lower edge of the
-        // bin where the count of those 4096 largest logits reaches k (of 4096, one
-        // seldom hides another of the first k).
-        if (set.top_k <= kMostK && floor < top) {
-            const float scale = count_scale(top, floor);
-#pragma unroll
-            for (int g = 0; g < 4; ++g)
-                if (own[g] > -INFINITY) count_logit(sh, own[g], top, scale);
-            __syncthreads();
-            const float from = count_edge(sh, set.top_k, top, floor, scale);
-            if (from > -INFINITY) {
-                // a wave takes about as long for one thread's place as for 64 threads' chunk
-                const uint32_t n = set.top_k <= 128 ? row.collect_from(sh, from, mine)
-                                                    : row.template collect<false>(sh, from, INFINITY);
-                if (n <= kList) return draw_from_list(sh, out, r, n, weight, set, least, from, uint32_t(row.v), value);
-            }
-        }
         cut.from_key(border_in_row<T>(sh, row, false, weight, -__FLT_MAX__, INFINITY, cut, uint64_t(set.top_k)));
         __syncthreads();
     }
@@ -1168,7 +1339,7 @@ __device__ __forceinline__ void sample_row(Shared &sh, const SampleArgs &args, i
         find_edges(sh, weight, top, b);
         __syncthreads();
         const float lo = sh.edge[0], hi = sh.edge[1];
-        const uint32_t n = cut_k || in_bin > 2 * kList ? kList + 1 : row.template collect<true>(sh, lo, hi);
+        const uint32_t n = cut_k || in_bin > 2 * kList ? kList + 1 : row.collect(sh, lo, fminf(next_below(hi), top));
         if (n > kList) {
             if (border.by_p)
                 cut.from_key(border_in_row<T>(sh, row, true, weight, lo, hi, cut, border.target - border.before));
@@ -1181,8 +1352,9 @@ __device__ __forceinline__ void sample_row(Shared &sh, const SampleArgs &args, i
     draw_from_row(sh, out, r, row, weight, set.u, cut);
 }
 
+// (at most 128 registers: 16 waves a CU in either form)
 template <typename T>
-__global__ __launch_bounds__(kThreads) void row_kernel(SampleArgs args, int64_t first) {
+__global__ __launch_bounds__(kThreads, 4) void row_kernel(SampleArgs args, int64_t first) {
     extern __shared__ __align__(16) char memory[];
     Shared &sh = *reinterpret_cast<Shared *>(memory);
     fill_factors(sh, args.shift);
