@@ -19,8 +19,8 @@ struct SampleArgs {
     int32_t *out_token;
     float *out_prob;
     int shift;  // weights are multiples of 2^-shift of the largest
-    // The quartic of Weights::unit with 2^shift multiplied in, 2^shift + 2^52, and
-    // 2^-shift: as arguments they reach the fmas in scalar registers.
+    // The quartic of Weights::units with 2^(shift - 1074) multiplied in, one that is
+    // 2^(shift - 1074), and 2^-shift: as arguments they reach the fmas in scalar registers.
     double c4, c3, c2, c1, one, per_unit;
 };
 

@@ -311,9 +311,10 @@ extern "C" rt_status rt_sample_rows(const void *logits, int32_t dtype, int64_t r
     while ((int64_t(1) << log2v) < v) ++log2v;
     const int shift = 62 - log2v < 46 ? 62 - log2v : 46;
     const double unit = double(int64_t(1) << shift);
-    const rt::SampleArgs a{logits,         r,         v,         ld,         u,           *settings,
-                           out_token,      out_prob,  shift,     rt::kC4 * unit, rt::kC3 * unit, rt::kC2 * unit,
-                           rt::kC1 * unit, unit + rt::kWhole, 1.0 / unit};
+    const double tiny = __builtin_ldexp(unit, -1074);
+    const rt::SampleArgs a{logits,         r,         v,    ld,         u,
+                           *settings,      out_token, out_prob, shift,  rt::kC4 * tiny,
+                           rt::kC3 * tiny, rt::kC2 * tiny, rt::kC1 * tiny, tiny, 1.0 / unit};
     hipStream_t s = static_cast<hipStream_t>(stream);
     hipError_t err;
     switch (dtype) {

@@ -117,8 +117,9 @@ struct Weights {
         const double p = power(x, &bin);
         return __builtin_bit_cast(uint64_t, fma_scalar(p, zero[bin], kWhole)) & 0x000fffffffffffffull;
     }
-    // For four elements: -bin, and 2^f alone in units of 2^-shift, for sums
-    // within one bin.
+    // For four elements: -bin, and 2^f alone in units of 2^-shift, for sums within
+    // one bin.  The polynomial is scaled by 2^-1074 besides: fp64 below 2^-1022 are
+    // whole multiples of that, and their bits are the multiple itself.
     __device__ __forceinline__ void units(const float *x, int *bin, uint64_t *unit) const {
         double octaves = kOctaves, lead = c4;
         asm("" : "+v"(octaves), "+v"(lead));  // an fma reads at most one scalar pair
@@ -136,7 +137,7 @@ struct Weights {
         fma_four(p, p, f, c1);
         fma_four(p, p, f, one);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) unit[e] = __builtin_bit_cast(uint64_t, p.v[e]) & 0x000fffffffffffffull;
+        for (int e = 0; e < 4; ++e) unit[e] = __builtin_bit_cast(uint64_t, p.v[e]);
     }
     __device__ __forceinline__ uint64_t whole(uint64_t sum, int bin) const {  // such a sum, with the bin's factor
         return bin ? uint64_t(__builtin_rint(double(sum) * (zero[-bin] * per_unit))) : sum;
