@@ -303,9 +303,10 @@ rt_status rt_quantize_rows_int8(const void *x, int32_t dtype, int64_t m, int32_t
                                 int64_t ldq, float *scale, void *stream);
 
 /*
- * out[i][j] = (sum_l a[i][l] b[j][l]) * a_scale[i] * b_scale[j] (+ bias[j]),
+ * out[i][j] = ((sum_l a[i][l] b[j][l]) * a_scale[i]) * b_scale[j] (+ bias[j]),
  * i < m, j < n: the sum is exact in 32-bit integers (int8 values -128..127,
- * k <= 65536), the rest fp32, rounded once to the output type.
+ * k <= 65536), the rest fp32 in this order (a scale above 2^97 can overflow with
+ * the largest sums), rounded once to the output type.
  *   a, b             device, m and n rows of k int8
  *   a_scale, b_scale device, m and n fp32;  bias  device, n fp32, or NULL
  *   out              device, m rows of n elements of out_dtype (fp32, bf16, fp16)
@@ -323,7 +324,7 @@ rt_status rt_matmul_int8(const int8_t *a, int64_t lda, const float *a_scale, con
  * rt_linear_int8_workspace(m, n, k) bytes, 16-byte aligned, that the call uses for
  * the quantised activations until its work on `stream` is done: calls that may
  * run at the same time (other streams, other graphs) need one each.
- * rt_linear_int8_workspace returns 0 where none is needed (m = 0, and a few short
+ * rt_linear_int8_workspace returns 0 where none is needed (m = 0, and few or short
  * activations, which one kernel takes whole), -1 for sizes the call refuses.
  */
 int64_t rt_linear_int8_workspace(int64_t m, int64_t n, int32_t k);
@@ -362,7 +363,8 @@ typedef struct {
  * weight; u < 0 or NaN: the first), and its probability w / S.  A row with no
  * logit above -inf gets token -1 and probability 0.
  * Sums are taken in 64-bit whole multiples of 2^-min(46, 62 - ceil(log2 v)) of
- * the largest weight: the same inputs always give the same token.
+ * the largest weight: the same inputs always give the same token.  A weight is
+ * within 2^-43 of itself and half such a unit; below 2^-47 of the largest it is 0.
  *   logits    device, r rows of v elements (fp32, bf16 or fp16), ld elements apart
  *   u         device, r fp32 in [0, 1)
  *   out_token device, r int32;  out_prob  device, r fp32, or NULL

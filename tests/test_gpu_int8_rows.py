@@ -220,7 +220,8 @@ def test_streams_and_graphs_with_a_workspace_each(m, n, k):
 @pytest.mark.parametrize("dtype", list(TYPES))
 @pytest.mark.parametrize("m,n,k", [(1, 77, 100), (1, 1024, 1024), (1, 8, 8192), (1, 300, 8193), (1, 8193, 64),
                                    (3, 500, 768), (4, 33, 2048), (4, 96, 4096), (5, 96, 1000), (31, 200, 777),
-                                   (80, 300, 640), (270, 530, 129)])
+                                   (80, 300, 640), (270, 530, 129), (33, 70, 1024), (8, 8192, 1024), (9, 8193, 1000),
+                                   (6, 40, 7), (8192, 20, 64), (40, 300, 1025)])
 def test_linear_is_quantize_then_product(dtype, m, n, k):
     g = torch.Generator().manual_seed(m + n + k)
     x = torch.randn(m, k, generator=g).to(TYPES[dtype]).cuda()
@@ -233,6 +234,36 @@ def test_linear_is_quantize_then_product(dtype, m, n, k):
     assert torch.equal(y, two)  # the same numbers as the two calls
     ws = torch.empty(max(1, linear_int8_workspace(m, n, k)), dtype=torch.uint8, device="cuda")
     assert torch.equal(y, linear_int8(x, w, sw, workspace=ws, out=torch.empty_like(y)))
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("m,n,k", [(40, 70, 777), (12, 33, 1024), (4, 50, 1000), (40, 70, 1100)])
+def test_linear_of_zero_tiny_tied_and_non_finite_rows(dtype, m, n, k):
+    """Rows that are quantised specially, out of a wider matrix, in every form of the one call."""
+    g = torch.Generator().manual_seed(m + k)
+    store = torch.full((m, k + 13), 1e4)
+    x = torch.randn(m, k, generator=g)
+    x[0] = 0.0
+    x[1] = 2.0 ** -126 if dtype == "fp32" else 2.0 ** -24
+    x[2] = (torch.randint(-127, 127, (k,), generator=g) + 0.5) / 2  # ties at a scale of one half
+    x[2, -1] = 63.5
+    x[3, k // 2] = float("inf")
+    if m > 4:
+        x[5, 0] = float("nan")
+        x[6] = (torch.randint(-127, 127, (k,), generator=g) + 0.5) / 2
+        x[6, 0] = -63.5
+        x[7, -1] = -float("inf")
+    store[:, 5:5 + k] = x
+    x = store.to(TYPES[dtype]).cuda()[:, 5:5 + k]
+    w, sw = int8_rows(n, k, g, k + 3, 1), scales(n, g)
+    bias = torch.randn(n, generator=g).cuda()
+    q, s = quantize_rows_int8(x)
+    e, es = row_oracle.quantize_rows(x.double().cpu().numpy())
+    assert np.array_equal(host(q), e) and np.array_equal(host(s), es.astype(np.float32), equal_nan=True)
+    y = linear_int8(x, w, sw, bias, out_dtype=torch.float32)
+    two = matmul_int8(q, s, w, sw, bias)
+    assert np.array_equal(host(y), host(two), equal_nan=True)
+    check(y, e, es.astype(np.float32), host(w), host(sw), host(bias))
 
 
 def test_empty_batch_and_scores_agree_with_rows():
@@ -307,8 +338,9 @@ def test_rejects_bad_tensors():
         linear_int8(x, w, sw, out=torch.empty(4, 5, device="cuda"))
     with pytest.raises(ValueError):
         linear_int8(x[0], w, sw)
+    assert linear_int8_workspace(9000, w.shape[0], 32) > 8
     with pytest.raises(ResidentTopKError):
-        linear_int8(torch.zeros(40, 32, device="cuda"), w, sw,
+        linear_int8(torch.zeros(9000, 32, device="cuda"), w, sw,
                     workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
     with pytest.raises(ResidentTopKError):
         linear_int8(torch.zeros(1, 70000, device="cuda"), torch.zeros(1, 70000, dtype=torch.int8, device="cuda"),

@@ -61,7 +61,7 @@ def test_linear_workspace(lib):
 
 
 def test_linear_refuses_before_anything_runs(lib):
-    def f(x=P, dt=F32, ldx=64, w=P, sw=P, out=P, odt=F32, ldo=20, m=400, n=20, k=64, ws=P, have=1 << 30):
+    def f(x=P, dt=F32, ldx=64, w=P, sw=P, out=P, odt=F32, ldo=20, m=9000, n=20, k=64, ws=P, have=1 << 30):
         return lib.rt_linear_int8(x, dt, ldx, w, 64, sw, NULL, out, odt, ldo, m, n, k, ws, have, NULL)
 
     for bad in (dict(x=NULL), dict(dt=0), dict(ldx=63), dict(w=NULL), dict(sw=ODD), dict(out=NULL), dict(odt=9),

@@ -10,7 +10,7 @@
 // are the first matrix operand and the activations the second, so that a
 // lane's four results are four neighbouring columns of one output row.
 //
-// Two kernels:
+// Products of int8 rows:
 //   tile    a workgroup's BM x BN outputs; 128-byte steps of both sides go
 //           straight from global memory to LDS (two buffers), swizzled so that
 //           the fragment reads spread over all banks.  For many activations.
@@ -19,6 +19,9 @@
 //           gives the same sum).  For few activations, where the rows b are
 //           read once and nothing is reused, and for rows that are not 16-byte
 //           aligned, which the LDS loads need.
+// Activations still to be quantised (rt_linear_int8): a kernel for that first, or,
+// where they are few or short and there is little else to do, in the same one:
+//   few     up to 4 activations; short  up to 1024 values and 256 workgroups.
 #include <hip/hip_runtime.h>
 
 #include "../../include/resident_topk.h"
@@ -63,21 +66,42 @@ __device__ __forceinline__ uint32_t magnitude(u32x4 v, uint32_t top) {
     for (int e = 0; e < int(16 / sizeof(T)); ++e) top = max(top, __float_as_uint(element<T>(v, e)) & 0x7fffffffu);
     return top;
 }
-// The codes of 16 bytes of T, 4 to a word.
+// The codes of 16 bytes of T, 4 to a word (0 where inv is).  Adding 1.5 * 2^23 to x
+// inv leaves the whole number n nearest to it in the low byte; it is the nearest
+// one to x / s, too, where |x - n s|, exact in one fma, stays below s / 2.  Where
+// any does not (a tie, or once in some hundred thousand the one beside it),
+// nearest_quotient decides.
 template <typename T>
 __device__ __forceinline__ void codes16(u32x4 v, float s, float inv, uint32_t (&w)[4 / sizeof(T)]) {
+    constexpr float kRound = 12582912.0f;
+    float off = 0.0f;
 #pragma unroll
     for (int g = 0; g < int(4 / sizeof(T)); ++g) {
-        w[g] = 0;
+        uint32_t n[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            w[g] |= (uint32_t(nearest_quotient(element<T>(v, g * 4 + e), s, inv)) & 0xffu) << (8 * e);
-        if (inv == 0.0f) w[g] = 0;
+        for (int e = 0; e < 4; ++e) {
+            const float x = element<T>(v, g * 4 + e), r = __builtin_fmaf(x, inv, kRound);
+            n[e] = __float_as_uint(r);
+            off = fmaxf(off, __builtin_fabsf(__builtin_fmaf(kRound - r, s, x)));
+        }
+        w[g] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(n[3], n[2], 0x0c0c0400u),
+                                     __builtin_amdgcn_perm(n[1], n[0], 0x0c0c0400u), 0x05040100u);
+    }
+    if (!(2.0f * off < s)) {
+#pragma unroll
+        for (int g = 0; g < int(4 / sizeof(T)); ++g) {
+            w[g] = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                w[g] |= (uint32_t(nearest_quotient(element<T>(v, g * 4 + e), s, inv)) & 0xffu) << (8 * e);
+            if (inv == 0.0f) w[g] = 0;
+        }
     }
 }
 
-// One workgroup per row: the largest magnitude, then the codes.  Bound by the read of x; the second pass takes up to
-// kQuantKeep chunks per thread from registers and the rest from L2.
+// One workgroup per row: the largest magnitude, then the codes; the second pass takes up to kQuantKeep chunks per
+// thread from registers and the rest from L2.  Bound by memory for many rows (8192 x 8192 bf16: 35 us, 5.7 TB/s
+// read and written; 2048 x 4096: 7.4 us), by latency for few (1 x 768: 2.6 us).
 template <typename T>
 __global__ __launch_bounds__(kQuantThreads) void quantize_kernel(const T *x, int64_t ldx, int64_t m, int k,
                                                                  int8_t *q, int64_t ldq, int kpad, float *scale) {
@@ -280,7 +304,7 @@ __global__ __launch_bounds__(64 * KW) void direct_kernel(Product p, int64_t tile
 // one launch (limits.hpp: int8_few).  Each workgroup of KW waves quantises all
 // of x into LDS while the first of its 16 rows b are on their way, then goes on
 // as the direct kernel.  Two launches cost a gap and a round trip of the codes
-// through memory: 1 x 4096 x 4096 6.4 us against 8.9, 1 x 1024 x 1024 4.3
+// through memory: 1 x 4096 x 4096 6.4 us against 8.9, 1 x 1024 x 1024 3.7
 // against 5.9; but every workgroup repeats the quantising (4 x 4096 x 4096: 10.9
 // against 9.3), hence the limit.
 template <int KW, typename T, typename O>
@@ -355,8 +379,124 @@ __global__ __launch_bounds__(64 * KW) void few_kernel(const T *x, int64_t ldx, P
     }
 }
 
+// The largest of the wave's 64 lanes, to all of them.
+__device__ __forceinline__ uint32_t wave_most(uint32_t v) {
+    v = max(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x111, 0xf, 0xf, false)));
+    v = max(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x112, 0xf, 0xf, false)));
+    v = max(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x114, 0xf, 0xf, false)));
+    v = max(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x118, 0xf, 0xf, false)));
+    v = max(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x142, 0xa, 0xf, false)));
+    v = max(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x143, 0xc, 0xf, false)));
+    return uint32_t(__builtin_amdgcn_readlane(int(v), 63));
+}
+
+// short: the same for activations of up to kInt8ShortK values, 32 of them and 32
+// rows b per workgroup of 16 waves: a wave takes every sixteenth activation, all of
+// whose values it holds at once, and then a 128-value block of the depth with half
+// of the rows b.  Up to one workgroup a CU it beats two launches (us, bf16, back to
+// back in a graph, with the calling path in brackets; fp32 alike):
+//   m x n x k            short         quantise + product
+//   8 x 1024 x 256       4.9 [8.4]     5.9 [12.6]
+//   77 x 1001 x 777      7.2 [8.5]     10.5 [12.8]
+//   256 x 1024 x 1024    7.6 [8.5]     8.2 [12.9]
+//   128 x 4096 x 256     7.8 [8.4]     7.0 [12.7]    512 workgroups: not taken
+//   512 x 1024 x 777     10.5 [10.5]   10.8 [12.7]   512 workgroups: not taken
+// What remains is latency: a launch, a round trip for x and b, the code's own way
+// into the instruction cache.
+template <typename T, typename O>
+__global__ __launch_bounds__(1024) void short_kernel(const T *x, int64_t ldx, Product p, int tiles_n) {
+    constexpr int NW = 16, MF = 2, NF = 2, KW = NW / NF, ROWS = MF * 16 / NW;
+    constexpr int E = 16 / sizeof(T), CH = kInt8ShortK / E / 64;  // 16-byte chunks a lane of each activation
+    extern __shared__ __align__(16) int8_t codes[];  // MF * 16 rows of kpad + 16 bytes
+    __shared__ i32x4 part[NW][MF][64];
+    __shared__ float scale[MF * 16];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r16 = lane & 15, g = lane >> 4;
+    const int64_t i0 = int64_t(blockIdx.x) / tiles_n * (MF * 16);
+    const int64_t j0 = int64_t(blockIdx.x) % tiles_n * (NF * 16) + wave / KW * 16;
+    const int m = int(min(p.m - i0, int64_t(MF * 16)));
+    const int stride = (p.k + 127) / 128 * 128 + 16;  // 16 more: neighbouring rows in other banks
+    const int whole = p.k / E, k0 = wave % KW * 128;
+
+    u32x4 keep[ROWS][CH];
+    float last[ROWS];  // a lane each for the values behind the whole chunks
+#pragma unroll
+    for (int h = 0; h < ROWS; ++h) {
+        const T *xr = x + (i0 + min(h * NW + wave, m - 1)) * ldx;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            keep[h][c] = u32x4{0, 0, 0, 0};
+            if (c * 64 + lane < whole) keep[h][c] = load16(xr + (c * 64 + lane) * E);
+        }
+        last[h] = lane < p.k - whole * E ? static_cast<float>(xr[whole * E + lane]) : 0.0f;
+    }
+    const int8_t *bp = p.b + min(j0 + r16, p.n - 1) * p.ldb + g * 16 + k0;
+    i32x4 b[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+    if (k0 + 128 <= p.k) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) b[s] = __builtin_bit_cast(i32x4, load16(bp + s * 64));
+    } else if (k0 < p.k) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) b[s] = load_part(bp + s * 64, p.k - k0 - s * 64 - g * 16, p.b_end());
+    }
+    uint32_t top[ROWS];
+#pragma unroll
+    for (int h = 0; h < ROWS; ++h) {
+        top[h] = __float_as_uint(last[h]) & 0x7fffffffu;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) top[h] = magnitude<T>(keep[h][c], top[h]);
+        top[h] = wave_most(top[h]);
+    }
+#pragma unroll
+    for (int h = 0; h < ROWS; ++h) {
+        float inv;
+        const float s = row_scale(top[h], &inv);
+        int8_t *row = codes + (h * NW + wave) * stride;
+        if (lane == 0) scale[h * NW + wave] = s;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            uint32_t w[4 / sizeof(T)];
+            codes16<T>(keep[h][c], s, inv, w);
+            if (c * 64 + lane < whole) __builtin_memcpy(row + (c * 64 + lane) * E, w, E);
+        }
+        for (int c = whole * E + lane; c < stride - 16; c += 64)
+            row[c] = c < p.k && inv != 0.0f ? int8_t(nearest_quotient(last[h], s, inv)) : int8_t(0);
+    }
+    __syncthreads();
+
+#pragma unroll
+    for (int h = 0; h < MF; ++h) {
+        i32x4 acc = {0, 0, 0, 0};
+        if (k0 < p.k) {
+            const int8_t *ap = codes + (h * 16 + r16) * stride + k0 + g * 16;
+#pragma unroll
+            for (int s = 0; s < 2; ++s) acc = mfma16(b[s], *reinterpret_cast<const i32x4 *>(ap + s * 64), acc);
+        }
+        part[wave][h][lane] = acc;
+    }
+    __syncthreads();
+    if (wave % KW < MF) {
+        const int h = wave % KW, w0 = wave - h;
+        i32x4 sum = part[w0][h][lane];
+#pragma unroll
+        for (int w = 1; w < KW; ++w) sum += part[w0 + w][h][lane];
+        const int i = h * 16 + r16;
+        const int64_t j = j0 + g * 4;
+        if (i < m && j < p.n) {
+            const int32_t s4[4] = {sum[0], sum[1], sum[2], sum[3]};
+            store_row<4, false, O>(p, i0 + i, j, s4, scale[i]);
+        }
+    }
+}
+
 template <typename T, typename O>
 hipError_t launch_few(const void *x, int64_t ldx, const Product &p, hipStream_t s) {
+    if (int8_short(p.m, p.n, p.k)) {
+        const int64_t tiles_n = (p.n + 31) / 32;
+        short_kernel<T, O><<<unsigned((p.m + 31) / 32 * tiles_n), 1024, size_t(int8_padded(p.k) + 16) * 32, s>>>(
+            static_cast<const T *>(x), ldx, p, int(tiles_n));
+        return hipGetLastError();
+    }
     const int64_t tiles = (p.n + 15) / 16;
     few_kernel<8, T, O><<<unsigned(tiles), 64 * 8, size_t(p.m) * size_t(int8_padded(p.k)), s>>>(
         static_cast<const T *>(x), ldx, p);

@@ -21,10 +21,14 @@ constexpr int64_t kMaxProduct = int64_t(1) << 37;
 constexpr int64_t int8_padded(int32_t k) { return (int64_t(k) + 127) / 128 * 128; }
 
 // Up to here rt_linear_int8 keeps the quantised activations in LDS and runs as
-// one kernel without a workspace (int8_rows.hip: few_kernel).
+// one kernel without a workspace (int8_rows.hip: few_kernel, short_kernel).
 constexpr int kInt8FewRows = 4, kInt8FewBytes = 8192, kInt8FewN = 8192;
+constexpr int kInt8ShortK = 1024, kInt8ShortTiles = 256;
+constexpr bool int8_short(int64_t m, int64_t n, int32_t k) {
+    return m > kInt8FewRows && k <= kInt8ShortK && (m + 31) / 32 * ((n + 31) / 32) <= kInt8ShortTiles;
+}
 constexpr bool int8_few(int64_t m, int64_t n, int32_t k) {
-    return m <= kInt8FewRows && m * int8_padded(k) <= kInt8FewBytes && n <= kInt8FewN;
+    return (m <= kInt8FewRows && m * int8_padded(k) <= kInt8FewBytes && n <= kInt8FewN) || int8_short(m, n, k);
 }
 
 // Row sampling: a few long rows are shared by up to kSampleSlices workgroups each
