@@ -32,16 +32,17 @@ constexpr bool int8_few(int64_t m, int64_t n, int32_t k) {
 }
 
 // Row sampling: a few long rows are shared by up to kSampleSlices workgroups each
-// (sample_rows.hip: split kernels), in slices of `per` chunks of 16 KiB.
+// (sample_rows.hip: split kernels), in slices of `per` chunks of kSplitChunk bytes.
 constexpr int kSampleSlices = 32;
 constexpr int64_t kSampleSlice = 33 * 1024;  // workspace bytes per slice
+constexpr int64_t kSplitChunk = 16384;
 constexpr int64_t kSplitLight = 1 << 20;  // bytes of a row from which top-k and greedy rows are shared, too
 struct Split {
     int slices, per;
 };
 constexpr Split sample_split(int64_t r, int64_t v, int64_t element) {
-    const int64_t chunks = (v * element + 16383) / 16384;
-    if (r < 1 || r > 16 || chunks < 16 || chunks < 4 * r) return Split{1, 0};
+    const int64_t chunks = (v * element + kSplitChunk - 1) / kSplitChunk;
+    if (r < 1 || r > 16 || chunks < 16) return Split{1, 0};
     int64_t most = 256 / r;  // one workgroup a CU
     most = most < kSampleSlices ? most : kSampleSlices;
     const int64_t per = (chunks + most - 1) / most;

@@ -273,25 +273,30 @@ template <typename T>
 hipError_t launch(const SampleArgs &a, int32_t dtype, void *workspace, hipStream_t s) {
     // Measured (us, one workgroup a row | slices; bf16, unless said):
     //   r x v                  no filter  top-p 0.95  min-p    top-k 50  greedy
-    //   1 x 65536              18 | 18    28 | 27     21 | 20  12 | 17   7 | 9
-    //   1 x 131072             27 | 18    40 | 30     31 | 20  14 | 18   10 | 9
-    //   8 x 131072             29 | 19    42 | 33     33 | 22  15 | 20   10 | 10
-    //   64 x 131072            30 | 31    43 | 44     33 | 31  15 | 20   11 | 12
-    //   1 x 1000000 fp32      180 | 24               188 | 28  43 | 22   74 | 11
+    //   1 x 32000 fp32         13 | 16    19 | 23    15 | 19   11 | 17   7 | 16
+    //   1 x 131072             26 | 18    37 | 30    25 | 19   12 | 19   9 | 16
+    //   8 x 131072             27 | 19    37 | 33    26 | 20   13 | 21   9 | 15
+    //   16 x 131072            27 | 19    38 | 37    26 | 20   13 | 22   9 | 15
+    //   64 x 131072            28 | 30    38 | 43    26 | 28   13 | 20   9 | 15
+    //   16 x 131072 fp32       30 | 19    39 | 34    34 | 24   14 | 21   13 | 15
+    //   1 x 1000000 fp32      163 | 30   685 | 88   169 | 28   41 | 22   75 | 15
+    // So top-k and greedy rows are shared from kSplitLight bytes on, the others
+    // always; where each row's top-k is its own (some may be off), few rows only.
     const Split split = sample_split(a.r, a.v, sizeof(T));
+    const int64_t bytes = a.v * int64_t(sizeof(T));
     const bool light = (a.set.top_ks == nullptr && a.set.top_k > 0) ||
                        (a.set.temperatures == nullptr && !(a.set.temperature > 0.0f));
-    if (split.slices > 1 && (!light || a.v * int64_t(sizeof(T)) >= kSplitLight))
-        return launch_split<T>(a, split, workspace, s);
+    const int64_t from = light ? kSplitLight : a.set.top_ks == nullptr ? 0 : 4 * kSplitChunk * a.r;
+    if (split.slices > 1 && bytes >= from) return launch_split<T>(a, split, workspace, s);
     // Measured (us, 1024 threads a row | 512, two rows a CU; bf16, unless said):
     //   r x v                 no filter  top-p 0.95  top-k 50  each its own
-    //   1 x 500 fp32           9 | 8     13 | 12     12 | 12    4 | 4
-    //   300 x 500 fp32        16 | 10    25 | 16     24 | 15   28 | 21
-    //   1 x 32000 fp32        15 | 14    21 | 21     12 | 14   15 | 13
-    //   256 x 32000           17 | 17    24 | 26     13 | 16   24 | 26
-    //   256 x 131072          38 | 44    54 | 61     20 | 23   46 | 58
-    //   512 x 32000           31 | 25    47 | 36     25 | 20   43 | 32
-    //   512 x 100000 fp32     77 | 79   109 | 107    49 | 50   82 | 78
+    //   1 x 500 fp32           9 | 8     13 | 12     12 | 11    7 | 7
+    //   300 x 500 fp32        17 | 10    25 | 16     24 | 15   24 | 18
+    //   1 x 32000 fp32        13 | 15    19 | 21     11 | 11    7 | 7
+    //   256 x 32000           15 | 15    22 | 22     11 | 13   21 | 21
+    //   256 x 131072          37 | 42    52 | 58     19 | 21   42 | 48
+    //   512 x 32000           28 | 22    41 | 31     22 | 17   40 | 28
+    //   512 x 100000 fp32     75 | 78   106 | 107    46 | 48   81 | 80
     if (a.r > 256 || a.v <= kList) return launch_rows_512(a, dtype, s);
     return launch_rows<T>(a, s);
 }
