@@ -101,7 +101,7 @@ def _output(o, out, dtype, m, n, like, device):
         code = o.floats.get(dtype)
         if code is None:
             raise TypeError(f"out_dtype must be torch.float32, torch.bfloat16 or torch.float16, got {dtype}")
-        return o.empty((m, n), dtype=dtype, device=like.device), code, n
+        return o.empty(m, n, dtype=dtype, device=like.device), code, n
     rows, cols, ld = _matrix(o, out, "out", o.floats, device)
     if rows != m or cols != n:
         raise ValueError(f"out must have shape [{m}, {n}], got {list(out.shape)}")
@@ -132,7 +132,7 @@ def quantize_rows_int8(x, out=None, out_scale=None, stream=None):
     m, k, ld = _matrix(o, x, "x", o.floats, device)
     if out is None:
         ldq = (k + 15) // 16 * 16
-        out = o.empty((m, ldq), dtype=o.int8, device=x.device)
+        out = o.empty(m, ldq, dtype=o.int8, device=x.device)
         if ldq != k:
             out[:, k:].zero_()
             out = out[:, :k]
