@@ -151,7 +151,7 @@ __global__ __launch_bounds__(kThreads) void split_border_kernel(SampleArgs args,
     const Weights weight = weights_of(sh, args, top, set.temperature);
     const float least = set.least(top);
     Own mass = {};
-    if (set.top_p < 1.0f && kOwn * t < kMass - 1)
+    if (set.top_p < 1.0f && kOwn * t < kNone)
         slice.each_slice([&](const Slice &one) { return *reinterpret_cast<const Own *>(one.mass + kOwn * t); }, Own{},
                          [&](const Own &m) {
 #pragma unroll
@@ -159,7 +159,7 @@ __global__ __launch_bounds__(kThreads) void split_border_kernel(SampleArgs args,
                          });
     const Border border = find_border(sh, weight, set, least, mass);
     double sum = 0.0;  // in a fixed order: 64-bit floating point is as good as whole numbers
-    for (int b = t; b < min(border.bin, kMass - 1); b += kThreads)
+    for (int b = t; b < min(border.bin, kNone); b += kThreads)
         sum = fma(double(slice.own->mass[b]), weight.zero[-b] * weight.per_unit, sum);
     const uint64_t kept = block_add(sh, uint64_t(__builtin_rint(sum)));
     if (border.bin < kMass) {

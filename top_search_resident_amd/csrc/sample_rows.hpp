@@ -27,7 +27,7 @@
 //       which segment the draw falls into; only that one is read again.
 //
 // What bounds it, in cycles of one workgroup of 1024 on 131072 bf16, top-p: the
-// histogram 35.7k of 76k (17 instructions a logit, 10 of them fp64, 4 cycles each),
+// histogram 33.4k of 73k (16 instructions a logit, 10 of them fp64, 4 cycles each),
 // passes 1 and 3 8k each from L2 (64 rows; 20k from the last-level cache with 256
 // rows, whose 67 MB pass L2's 4 MB an XCD), the searches 3.5k each (a barrier or a
 // memory's round trip after the other, which the waves spend waiting).  Short rows,
@@ -62,19 +62,21 @@ constexpr int kPlaces = 4096; // 16-byte places that hold candidates
 // ------------------------------------------------------------------- weights
 
 // exp((x - top) / T) as a whole multiple of 2^-shift.  In octaves, t = (x - top)
-// log2(e) / T = 47 (sigma - 1), with sigma clamped to [0, 1], which an fma does
-// at no cost: NaN gives 0, as anything 47 octaves or more down (weight 0).  Adding
-// 1.5 * 2^47 leaves round(32 t) in the low bits, -bin; the rest f (|f| <= 2^-6)
-// gives 2^f by a quartic fitted with its constant fixed at 1 (relative error
-// 2^-43.5), and a table in LDS the factor 2^(shift - bin / 32), 0 in the last
-// bin; adding 2^52 rounds to a whole number.  The largest logit is finite here
-// (a row whose largest is +inf takes draw_infinite).
-constexpr int kPerOctave = 32, kOctaves = 47, kMass = kOctaves * kPerOctave + 1;
+// log2(e) / T = 49 (sigma - 1), with sigma clamped to [0, 1], which an fma does
+// at no cost: NaN gives 0, as anything 49 octaves or more down.  Adding 1.5 * 2^47
+// leaves round(32 t) in the low bits, -bin; the rest f (|f| <= 2^-6) gives 2^f by
+// a quartic fitted with its constant fixed at 1 (relative error 2^-43.5), and a
+// table in LDS the factor 2^(shift - bin / 32), 0 from 47 octaves on; adding 2^52
+// rounds to a whole number.  The largest logit is finite here (a row whose
+// largest is +inf takes draw_infinite).
+//
+// The two octaves without weight are room: elements that have none would all add
+// to the last bin of the histogram, one after the other.  Each adds to the lane's
+// own of the last 64 bins instead, which takes one maximum of two whole numbers.
+constexpr int kPerOctave = 32, kOctaves = 49, kMass = kOctaves * kPerOctave + 1;
+constexpr int kNone = kMass - 1 - 64;  // bins from here on have no weight
 constexpr double kRound = 211106232532992.0;   // 1.5 * 2^47
 constexpr double kWhole = 4503599627370496.0;  // 2^52
-// Elements without weight would all add to one bin: they go to one of these by lane.
-constexpr int kSpread = 64, kStride = kMass + kSpread;
-
 typedef const __attribute__((address_space(3))) double *lds_doubles;
 
 // a b + c with c in scalar registers.  Written out because the compiler turns an
@@ -191,7 +193,7 @@ struct Cut {
 // ------------------------------------------------------------- block helpers
 
 struct Shared {
-    uint64_t bin[kSegs * kStride];
+    uint64_t bin[kSegs * kMass];
     uint64_t list[kList];
     uint64_t weight[kSmall];
     double factor[kMass];
@@ -202,7 +204,7 @@ struct Shared {
     float f[kWaves], g[kWaves];
     float edge[2];
 };
-static_assert(kSearch <= kSegs * kStride && kPlaces / 2 <= kSegs * kStride, "find_first uses the histograms' memory");
+static_assert(kSearch <= kSegs * kMass && kPlaces / 2 <= kSegs * kMass, "find_first uses the histograms' memory");
 
 typedef unsigned long long ull;
 __device__ __forceinline__ void add64(uint64_t *p, uint64_t v) {
@@ -1006,7 +1008,7 @@ __device__ __forceinline__ void draw_from_row(Shared &sh, Output out, int64_t r,
     row.each(
         [&](float y, uint32_t i) {
             double f;
-            if (cut(y, i) && weight.split(y, &f) > 1 - kMass) {
+            if (cut(y, i) && weight.split(y, &f) > -kNone) {
                 const uint64_t key = (uint64_t(weight(y) != 0) << 32) | i;
                 behind = key > behind ? key : behind;
             }
@@ -1082,7 +1084,7 @@ __device__ __forceinline__ void draw_infinite(Shared &sh, Output out, int64_t r,
     if (threadIdx.x == 0) write_row(out, r, key_index(key), float(1.0 / double(n)));
 }
 
-// The smallest fp32 whose bin is at most b < kMass - 1, by one wave, which tries
+// The smallest fp32 whose bin is at most b < kNone, by one wave, which tries
 // 64 values at once: those around where the bin's edge lies in real numbers,
 // and, where that fails (next to zero fp32 is finer than the 64-bit logits'
 // rounding), a 64th of what is left at a time.
@@ -1111,10 +1113,10 @@ __device__ __forceinline__ float bin_edge(const Weights &weight, float top, int 
 // The histograms of the weights of what `inside` keeps.
 template <int SEGS, typename T, typename Inside>
 __device__ __forceinline__ void mass_histogram(Shared &sh, const Row<T> &row, const Weights &weight, Inside inside) {
-    for (int i = threadIdx.x; i < SEGS * kStride; i += kThreads) sh.bin[i] = 0;
+    for (int i = threadIdx.x; i < SEGS * kMass; i += kThreads) sh.bin[i] = 0;
     __syncthreads();
     // bin b of a segment is at [kMass - 1 - b]
-    const int spread = kMass - (kMass - 1) + int(threadIdx.x & 63);
+    const int spread = int(threadIdx.x & 63) - (kMass - 1);
     uint64_t *bins = sh.bin + kMass - 1;
     int left = row.per;
     row.each_chunk(
@@ -1130,11 +1132,11 @@ __device__ __forceinline__ void mass_histogram(Shared &sh, const Row<T> &row, co
                 weight.units(y, b, unit);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const bool in = (b[e] > 1 - kMass) & inside(y[e], i + h * 4 + e);
-                    add64(bins + (in ? b[e] : spread), unit[e]);
+                    const int at = inside(y[e], i + h * 4 + e) ? b[e] : spread;
+                    add64(bins + max(at, spread), unit[e]);
                 }
             }
-            if (--left == 0) bins += kStride, left = row.per;
+            if (--left == 0) bins += kMass, left = row.per;
         });
     __syncthreads();
 }
@@ -1149,7 +1151,7 @@ __device__ __forceinline__ void fill_factors(Shared &sh, int shift) {
     // a thread's bins are kThreads apart, whole octaves: one power for all of them
     const double part = exp2(double(threadIdx.x % kPerOctave) / -kPerOctave);
     for (int b = threadIdx.x; b < kMass; b += kThreads)
-        sh.factor[kMass - 1 - b] = b < kMass - 1 ? __builtin_ldexp(part, shift - b / kPerOctave) : 0.0;
+        sh.factor[kMass - 1 - b] = b < kNone ? __builtin_ldexp(part, shift - b / kPerOctave) : 0.0;
 }
 
 // Counts x, at least floor, in the bins of [floor, top].
@@ -1185,7 +1187,7 @@ __device__ __forceinline__ Border find_border(Shared &sh, const Weights &weight,
 #pragma unroll
         for (int i = 0; i < kOwn; ++i) {
             const int bin = kOwn * threadIdx.x + i;
-            own.v[i] = bin < kMass - 1 ? weight.whole(own.v[i], bin) : 0;
+            own.v[i] = bin < kNone ? weight.whole(own.v[i], bin) : 0;
         }
         border.bin = find_bin(sh, own, [&](uint64_t all) { return at_least(set.top_p, all); }, &border.before,
                               &border.target);
@@ -1196,7 +1198,7 @@ __device__ __forceinline__ Border find_border(Shared &sh, const Weights &weight,
         const int l = -weight.split(least, &f);
         if (l < border.bin) border.by_p = false, border.bin = l;
     }
-    if (border.bin >= kMass - 1) border.bin = kMass, border.by_p = false;
+    if (border.bin >= kNone) border.bin = kMass, border.by_p = false;
     return border;
 }
 
@@ -1318,11 +1320,11 @@ __device__ __forceinline__ void sample_row(Shared &sh, const SampleArgs &args, i
     else
         mass_histogram<kSegs>(sh, row, weight, [](float, uint32_t) { return true; });
     Own mass = {};
-    if (set.top_p < 1.0f && kOwn * t < kMass - 1) {
+    if (set.top_p < 1.0f && kOwn * t < kNone) {
 #pragma unroll
         for (int s = 0; s < kSegs; ++s)
 #pragma unroll
-            for (int i = 0; i < kOwn; ++i) mass.v[i] += sh.bin[s * kStride + kMass - 1 - kOwn * t - i];
+            for (int i = 0; i < kOwn; ++i) mass.v[i] += sh.bin[s * kMass + kMass - 1 - kOwn * t - i];
     }
     const Border border = find_border(sh, weight, set, least, mass);
     const int b = border.bin;
@@ -1330,7 +1332,7 @@ __device__ __forceinline__ void sample_row(Shared &sh, const SampleArgs &args, i
     uint64_t in_bin = 0;
     if (b < kMass) {
 #pragma unroll
-        for (int s = 0; s < kSegs; ++s) in_bin += sh.bin[s * kStride + kMass - 1 - b];
+        for (int s = 0; s < kSegs; ++s) in_bin += sh.bin[s * kMass + kMass - 1 - b];
         in_bin >>= args.shift;
     }
     if (t < kSlices) sh.seg[t] = 0;
@@ -1340,8 +1342,8 @@ __device__ __forceinline__ void sample_row(Shared &sh, const SampleArgs &args, i
         constexpr int kEach = kThreads / kSegs;
         const int s = t / kEach;
         double sum = 0.0;
-        for (int i = t % kEach; i < min(b, kMass - 1); i += kEach)
-            sum = fma(double(sh.bin[s * kStride + kMass - 1 - i]), weight.zero[-i] * weight.per_unit, sum);
+        for (int i = t % kEach; i < min(b, kNone); i += kEach)
+            sum = fma(double(sh.bin[s * kMass + kMass - 1 - i]), weight.zero[-i] * weight.per_unit, sum);
         const uint64_t all = wave_add(uint64_t(__builtin_rint(sum)));
         if ((t & 63) == 0) add64(&sh.seg[s], all);
     }
