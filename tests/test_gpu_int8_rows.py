@@ -221,7 +221,8 @@ def test_streams_and_graphs_with_a_workspace_each(m, n, k):
 @pytest.mark.parametrize("m,n,k", [(1, 77, 100), (1, 1024, 1024), (1, 8, 8192), (1, 300, 8193), (1, 8193, 64),
                                    (3, 500, 768), (4, 33, 2048), (4, 96, 4096), (5, 96, 1000), (31, 200, 777),
                                    (80, 300, 640), (270, 530, 129), (33, 70, 1024), (8, 8192, 1024), (9, 8193, 1000),
-                                   (6, 40, 7), (8192, 20, 64), (40, 300, 1025)])
+                                   (6, 40, 7), (8192, 20, 64), (40, 300, 1025), (1, 9000, 1024), (1, 20011, 1000),
+                                   (1, 8300, 9), (2, 8333, 500), (4, 9001, 250), (1, 8200, 1025)])
 def test_linear_is_quantize_then_product(dtype, m, n, k):
     g = torch.Generator().manual_seed(m + n + k)
     x = torch.randn(m, k, generator=g).to(TYPES[dtype]).cuda()
@@ -237,7 +238,7 @@ def test_linear_is_quantize_then_product(dtype, m, n, k):
 
 
 @pytest.mark.parametrize("dtype", list(TYPES))
-@pytest.mark.parametrize("m,n,k", [(40, 70, 777), (12, 33, 1024), (4, 50, 1000), (40, 70, 1100)])
+@pytest.mark.parametrize("m,n,k", [(40, 70, 777), (12, 33, 1024), (4, 50, 1000), (40, 70, 1100), (4, 8300, 200)])
 def test_linear_of_zero_tiny_tied_and_non_finite_rows(dtype, m, n, k):
     """Rows that are quantised specially, out of a wider matrix, in every form of the one call."""
     g = torch.Generator().manual_seed(m + k)

@@ -21,7 +21,8 @@
 //           aligned, which the LDS loads need.
 // Activations still to be quantised (rt_linear_int8): a kernel for that first, or,
 // where they are few or short and there is little else to do, in the same one:
-//   few     up to 4 activations; short  up to 1024 values and 256 workgroups.
+//   few     up to 4 activations;  stream  one or two short ones, many rows b;
+//   short   up to 1024 values each and 256 workgroups.
 #include <hip/hip_runtime.h>
 
 #include "../../include/resident_topk.h"
@@ -300,36 +301,20 @@ __global__ __launch_bounds__(64 * KW) void direct_kernel(Product p, int64_t tile
     }
 }
 
-// few: rt_linear_int8 of a few short activations against not too many rows in
-// one launch (limits.hpp: int8_few).  Each workgroup of KW waves quantises all
-// of x into LDS while the first of its 16 rows b are on their way, then goes on
-// as the direct kernel.  Two launches cost a gap and a round trip of the codes
-// through memory: 1 x 4096 x 4096 6.4 us against 8.9, 1 x 1024 x 1024 3.7
-// against 5.9; but every workgroup repeats the quantising (4 x 4096 x 4096: 10.9
-// against 9.3), hence the limit.
-template <int KW, typename T, typename O>
-__global__ __launch_bounds__(64 * KW) void few_kernel(const T *x, int64_t ldx, Product p) {
+// m rows of x by the whole workgroup of KW waves: their codes, and zeros up to kpad,
+// into LDS, the bits of their largest magnitudes into top.
+template <int KW, typename T>
+__device__ __forceinline__ void quantize_to_lds(const T *x, int64_t ldx, int m, int k, int kpad, int8_t *codes,
+                                                uint32_t *top) {
     constexpr int E = 16 / sizeof(T), kThreads = 64 * KW;
-    extern __shared__ __align__(16) int8_t codes[];  // m rows of kpad bytes
-    __shared__ i32x4 part[KW][64];
-    __shared__ uint32_t top[kInt8FewRows];
-    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-    const int r16 = lane & 15, g = lane >> 4;
-    const int m = int(p.m), kpad = (p.k + 127) / 128 * 128, whole = p.k / E, blocks = p.k / 128;
-    const int8_t *bp = p.b + min(blockIdx.x * int64_t(16) + r16, p.n - 1) * p.ldb + g * 16;
-
-    i32x4 b0 = {0, 0, 0, 0}, b1 = {0, 0, 0, 0};
-    if (wave < blocks) {
-        b0 = __builtin_bit_cast(i32x4, load16(bp + wave * 128));
-        b1 = __builtin_bit_cast(i32x4, load16(bp + wave * 128 + 64));
-    }
+    const int t = threadIdx.x, lane = t & 63, whole = k / E;
     if (t < kInt8FewRows) top[t] = 0;
     __syncthreads();
     for (int i = 0; i < m; ++i) {
         const T *xr = x + i * ldx;
         uint32_t own = 0;
         for (int c = t; c < whole; c += kThreads) own = magnitude<T>(load16(xr + c * E), own);
-        if (t < p.k - whole * E) own = max(own, __float_as_uint(static_cast<float>(xr[whole * E + t])) & 0x7fffffffu);
+        if (t < k - whole * E) own = max(own, __float_as_uint(static_cast<float>(xr[whole * E + t])) & 0x7fffffffu);
 #pragma unroll
         for (int o = 32; o > 0; o >>= 1) own = max(own, uint32_t(__shfl_xor(int(own), o)));
         if (lane == 0) atomicMax(&top[i], own);
@@ -346,9 +331,34 @@ __global__ __launch_bounds__(64 * KW) void few_kernel(const T *x, int64_t ldx, P
         }
         for (int c = whole * E + t; c < kpad; c += kThreads)
             codes[i * kpad + c] =
-                c < p.k && inv != 0.0f ? int8_t(nearest_quotient(static_cast<float>(xr[c]), s, inv)) : int8_t(0);
+                c < k && inv != 0.0f ? int8_t(nearest_quotient(static_cast<float>(xr[c]), s, inv)) : int8_t(0);
     }
     __syncthreads();
+}
+
+// few: rt_linear_int8 of a few short activations against not too many rows in
+// one launch (limits.hpp: int8_few).  Each workgroup of KW waves quantises all
+// of x into LDS while the first of its 16 rows b are on their way, then goes on
+// as the direct kernel.  Two launches cost a gap and a round trip of the codes
+// through memory: 1 x 4096 x 4096 6.4 us against 8.9, 1 x 1024 x 1024 3.7
+// against 5.9; but every workgroup repeats the quantising (4 x 4096 x 4096: 10.9
+// against 9.3), hence the limit.
+template <int KW, typename T, typename O>
+__global__ __launch_bounds__(64 * KW) void few_kernel(const T *x, int64_t ldx, Product p) {
+    extern __shared__ __align__(16) int8_t codes[];  // m rows of kpad bytes
+    __shared__ i32x4 part[KW][64];
+    __shared__ uint32_t top[kInt8FewRows];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int r16 = lane & 15, g = lane >> 4;
+    const int m = int(p.m), kpad = (p.k + 127) / 128 * 128, blocks = p.k / 128;
+    const int8_t *bp = p.b + min(blockIdx.x * int64_t(16) + r16, p.n - 1) * p.ldb + g * 16;
+
+    i32x4 b0 = {0, 0, 0, 0}, b1 = {0, 0, 0, 0};
+    if (wave < blocks) {
+        b0 = __builtin_bit_cast(i32x4, load16(bp + wave * 128));
+        b1 = __builtin_bit_cast(i32x4, load16(bp + wave * 128 + 64));
+    }
+    quantize_to_lds<KW>(x, ldx, m, p.k, kpad, codes, top);
 
     const int8_t *ap = codes + min(r16, m - 1) * kpad + g * 16;
     i32x4 acc = {0, 0, 0, 0};
@@ -376,6 +386,57 @@ __global__ __launch_bounds__(64 * KW) void few_kernel(const T *x, int64_t ldx, P
             const int32_t s4[4] = {sum[0], sum[1], sum[2], sum[3]};
             store_row<4, false, O>(p, r16, j, s4, row_scale(top[r16], &inv));
         }
+    }
+}
+
+// stream: the same against many rows b.  A wave takes 16 of them over the whole
+// depth, the first half a KiB of each on its way while x is quantised, so that
+// the reads of b start with the kernel and nothing is joined at the end.  Bound by
+// them (1 x 262144 x 768: 5.8 TB/s).  For one or two activations of up to 1024
+// values together it beats two launches (us, bf16, fp32 out, back to back in a
+// graph):
+//   m x n x k            stream   quantise + product
+//   1 x 16384 x 768      6.2      6.9
+//   1 x 100000 x 768     17.3     18.9
+//   1 x 100000 x 777     19.4     26.7
+//   2 x 100000 x 512     14.0     16.0
+//   4 x 100000 x 250     15.5     14.1    not taken
+//   1 x 16384 x 4096     18.4     15.2    not taken
+template <typename T, typename O>
+__global__ __launch_bounds__(512) void stream_kernel(const T *x, int64_t ldx, Product p) {
+    constexpr int KW = 8, DEEP = 8;
+    extern __shared__ __align__(16) int8_t codes[];  // m rows of kpad bytes
+    __shared__ uint32_t top[kInt8FewRows];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int r16 = lane & 15, g = lane >> 4;
+    const int m = int(p.m), kpad = (p.k + 127) / 128 * 128, steps = p.k / 64;
+    const int64_t j0 = (blockIdx.x * int64_t(KW) + wave) * 16;
+    const int8_t *bp = p.b + min(j0 + r16, p.n - 1) * p.ldb + g * 16;
+    i32x4 b[DEEP];
+    const auto fetch = [&](int s0) {
+#pragma unroll
+        for (int i = 0; i < DEEP; ++i)
+            if (s0 + i < steps) b[i] = __builtin_bit_cast(i32x4, load16(bp + (s0 + i) * 64));
+    };
+    fetch(0);
+    quantize_to_lds<KW>(x, ldx, m, p.k, kpad, codes, top);
+
+    const int8_t *ap = codes + min(r16, m - 1) * kpad + g * 16;
+    i32x4 acc = {0, 0, 0, 0};
+    for (int s0 = 0; s0 < steps; s0 += DEEP) {
+        if (s0 > 0) fetch(s0);
+#pragma unroll
+        for (int i = 0; i < DEEP; ++i)
+            if (s0 + i < steps) acc = mfma16(b[i], *reinterpret_cast<const i32x4 *>(ap + (s0 + i) * 64), acc);
+    }
+    if (steps * 64 < p.k)  // the codes behind the depth are 0
+        acc = mfma16(load_part(bp + steps * 64, p.k - steps * 64 - g * 16, p.b_end()),
+                     *reinterpret_cast<const i32x4 *>(ap + steps * 64), acc);
+    const int64_t j = j0 + g * 4;
+    float inv;
+    if (r16 < m && j < p.n) {
+        const int32_t s4[4] = {acc[0], acc[1], acc[2], acc[3]};
+        store_row<4, false, O>(p, r16, j, s4, row_scale(top[r16], &inv));
     }
 }
 
@@ -495,6 +556,11 @@ hipError_t launch_few(const void *x, int64_t ldx, const Product &p, hipStream_t 
         const int64_t tiles_n = (p.n + 31) / 32;
         short_kernel<T, O><<<unsigned((p.m + 31) / 32 * tiles_n), 1024, size_t(int8_padded(p.k) + 16) * 32, s>>>(
             static_cast<const T *>(x), ldx, p, int(tiles_n));
+        return hipGetLastError();
+    }
+    if (p.n > kInt8FewN) {
+        stream_kernel<T, O><<<unsigned((p.n + 127) / 128), 512, size_t(p.m) * size_t(int8_padded(p.k)), s>>>(
+            static_cast<const T *>(x), ldx, p);
         return hipGetLastError();
     }
     const int64_t tiles = (p.n + 15) / 16;

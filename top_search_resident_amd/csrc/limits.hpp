@@ -21,14 +21,19 @@ constexpr int64_t kMaxProduct = int64_t(1) << 37;
 constexpr int64_t int8_padded(int32_t k) { return (int64_t(k) + 127) / 128 * 128; }
 
 // Up to here rt_linear_int8 keeps the quantised activations in LDS and runs as
-// one kernel without a workspace (int8_rows.hip: few_kernel, short_kernel).
+// one kernel without a workspace (int8_rows.hip: few_kernel, stream_kernel for more
+// rows b, short_kernel for more activations).
 constexpr int kInt8FewRows = 4, kInt8FewBytes = 8192, kInt8FewN = 8192;
+constexpr int kInt8StreamRows = 2, kInt8StreamBytes = 1024;
+constexpr int64_t kInt8StreamN = int64_t(1) << 29;  // fewer than 2^32 threads
 constexpr int kInt8ShortK = 1024, kInt8ShortTiles = 256;
 constexpr bool int8_short(int64_t m, int64_t n, int32_t k) {
     return m > kInt8FewRows && k <= kInt8ShortK && (m + 31) / 32 * ((n + 31) / 32) <= kInt8ShortTiles;
 }
 constexpr bool int8_few(int64_t m, int64_t n, int32_t k) {
-    return (m <= kInt8FewRows && m * int8_padded(k) <= kInt8FewBytes && n <= kInt8FewN) || int8_short(m, n, k);
+    const int64_t bytes = m * int8_padded(k);
+    return (m <= kInt8FewRows && bytes <= kInt8FewBytes && n <= kInt8FewN) ||
+           (m <= kInt8StreamRows && bytes <= kInt8StreamBytes && n <= kInt8StreamN) || int8_short(m, n, k);
 }
 
 // Row sampling: a few long rows are shared by up to kSampleSlices workgroups each
