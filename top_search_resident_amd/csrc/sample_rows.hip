@@ -312,14 +312,9 @@ extern "C" rt_status rt_sample_rows(const void *logits, int32_t dtype, int64_t r
     rt_status st = rt_check_sample_rows(logits, dtype, r, v, ld, u, settings, out_token, out_prob, workspace,
                                         workspace_bytes);
     if (st != RT_OK || r == 0) return st;
-    int log2v = 0;
-    while ((int64_t(1) << log2v) < v) ++log2v;
-    const int shift = 62 - log2v < 46 ? 62 - log2v : 46;
-    const double unit = double(int64_t(1) << shift);
-    const double tiny = __builtin_ldexp(unit, -1074);
-    const rt::SampleArgs a{logits,         r,         v,    ld,         u,
-                           *settings,      out_token, out_prob, shift,  rt::kC4 * tiny,
-                           rt::kC3 * tiny, rt::kC2 * tiny, rt::kC1 * tiny, tiny, 1.0 / unit};
+    const int shift = rt::sample_shift(v);
+    const rt::SampleArgs a{logits, r, v, ld, u, *settings, out_token, out_prob, shift, rt::sample_units(shift),
+                           1.0 / double(int64_t(1) << shift)};
     hipStream_t s = static_cast<hipStream_t>(stream);
     hipError_t err;
     switch (dtype) {

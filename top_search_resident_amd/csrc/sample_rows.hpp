@@ -129,8 +129,8 @@ struct Weights {
         return __builtin_bit_cast(uint64_t, fma_scalar(p, zero[bin], kWhole)) & 0x000fffffffffffffull;
     }
     // For four elements: -bin, and 2^f alone in units of 2^-shift, for sums within
-    // one bin.  The polynomial is scaled by 2^-1074 besides: fp64 below 2^-1022 are
-    // whole multiples of that, and their bits are the multiple itself.
+    // one bin.  The polynomial is scaled by 2^-1074 besides (sample_units.hpp): fp64
+    // below 2^-1022 are whole multiples of that, and their bits are the multiple itself.
     __device__ __forceinline__ void units(const float *x, int *bin, uint64_t *unit) const {
         double octaves = kOctaves, lead = c4;
         asm("" : "+v"(octaves), "+v"(lead));  // an fma reads at most one scalar pair
@@ -313,11 +313,11 @@ __device__ __forceinline__ uint64_t at_least(float part, uint64_t whole) {
     return n < 1 ? 1 : (n > whole ? whole : n);
 }
 
-// The least number of units above u of `whole`.
+// The least number of units above u of `whole`; never more than `whole`, so that
+// some running sum always reaches it.
 __device__ __forceinline__ uint64_t above(float u, uint64_t whole) {
-    if (!(u > 0.0f)) return 1;
     if (u >= 1.0f) return whole;
-    const uint64_t n = uint64_t(double(u) * double(whole)) + 1;
+    const uint64_t n = u > 0.0f ? uint64_t(double(u) * double(whole)) + 1 : 1;
     return n > whole ? whole : n;
 }
 
@@ -1143,7 +1143,13 @@ __device__ __forceinline__ void mass_histogram(Shared &sh, const Row<T> &row, co
 
 __device__ __forceinline__ Weights weights_of(Shared &sh, const SampleArgs &args, float top, float temperature) {
     return Weights{double(top), 1.4426950408889634 / kOctaves / double(temperature),
-                   (lds_doubles)(sh.factor + kMass - 1), args.c4, args.c3, args.c2, args.c1, args.one, args.per_unit};
+                   (lds_doubles)(sh.factor + kMass - 1),
+                   __builtin_bit_cast(double, args.units.c4),
+                   __builtin_bit_cast(double, args.units.c3),
+                   __builtin_bit_cast(double, args.units.c2),
+                   __builtin_bit_cast(double, args.units.c1),
+                   __builtin_bit_cast(double, args.units.one),
+                   args.per_unit};
 }
 
 // The factors' table; a barrier follows before its first use.
