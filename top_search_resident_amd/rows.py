@@ -95,9 +95,11 @@ def _vector(o, t, name, dtype, n, device):
     return t.data_ptr()
 
 
-def _output(o, out, dtype, m, n, like, device):
-    """(out, its type's code, its row stride), made here where none is given."""
+def _output(o, out, dtype, default, m, n, like, device):
+    """(out, its type's code, its row stride), made here where none is given, of type
+    `dtype` (None: out's own, or `default`)."""
     if out is None:
+        dtype = default if dtype is None else dtype
         code = o.floats.get(dtype)
         if code is None:
             raise TypeError(f"out_dtype must be torch.float32, torch.bfloat16 or torch.float16, got {dtype}")
@@ -105,6 +107,8 @@ def _output(o, out, dtype, m, n, like, device):
     rows, cols, ld = _matrix(o, out, "out", o.floats, device)
     if rows != m or cols != n:
         raise ValueError(f"out must have shape [{m}, {n}], got {list(out.shape)}")
+    if dtype is not None and dtype != out.dtype:
+        raise TypeError(f"out is {out.dtype}, out_dtype {dtype}")
     return out, o.floats[out.dtype], ld
 
 
@@ -152,8 +156,8 @@ def quantize_rows_int8(x, out=None, out_scale=None, stream=None):
 def matmul_int8(a, a_scale, b, b_scale, bias=None, out=None, out_dtype=None, stream=None):
     """out[i, j] = sum(a[i] * b[j]) * a_scale[i] * b_scale[j] (+ bias[j]) for int8
     rows a [m, k] and b [n, k] with fp32 scales [m] and [n] and an fp32 bias [n].
-    The sums are exact; the result is rounded once to out_dtype (default fp32), fp32, bf16
-    or fp16.  Returns out [m, n]."""
+    The sums are exact; the result is rounded once to out_dtype (fp32, bf16 or fp16;
+    default: out's type, or fp32).  Returns out [m, n]."""
     o = _once if _once.lib else _once.load()
     context = _elsewhere(o, a, "a", stream)
     if context is not None:
@@ -167,7 +171,7 @@ def matmul_int8(a, a_scale, b, b_scale, bias=None, out=None, out_dtype=None, str
     sa = _vector(o, a_scale, "a_scale", o.fp32, m, device)
     sb = _vector(o, b_scale, "b_scale", o.fp32, n, device)
     pbias = None if bias is None else _vector(o, bias, "bias", o.fp32, n, device)
-    out, code, ldo = _output(o, out, out_dtype or o.fp32, m, n, a, device)
+    out, code, ldo = _output(o, out, out_dtype, o.fp32, m, n, a, device)
     st = o.lib.rt_matmul_int8(a.data_ptr(), lda, sa, b.data_ptr(), ldb, sb, pbias, out.data_ptr(), code, ldo, m, n, k,
                               o.stream(device))
     if st:
@@ -178,7 +182,7 @@ def matmul_int8(a, a_scale, b, b_scale, bias=None, out=None, out_dtype=None, str
 def linear_int8(x, w, w_scale, bias=None, out=None, out_dtype=None, workspace=None, stream=None):
     """matmul_int8(*quantize_rows_int8(x), w, w_scale, bias): activations x [m, k]
     (fp32, bf16 or fp16), quantised row by row, times int8 rows w [n, k].  Returns
-    out [m, n] in out_dtype (default: x's type).  `workspace`: a uint8 CUDA tensor
+    out [m, n] in out_dtype (default: out's type, or x's).  `workspace`: a uint8 CUDA tensor
     of at least linear_int8_workspace(m, n, k) bytes, 16-byte aligned, for callers
     that keep one (one for each call that may run at the same time); by default
     one is taken from torch's allocator for the call."""
@@ -194,7 +198,7 @@ def linear_int8(x, w, w_scale, bias=None, out=None, out_dtype=None, workspace=No
         raise ValueError(f"x has rows of {k}, w rows of {kw}")
     sw = _vector(o, w_scale, "w_scale", o.fp32, n, device)
     pbias = None if bias is None else _vector(o, bias, "bias", o.fp32, n, device)
-    out, code, ldo = _output(o, out, out_dtype or x.dtype, m, n, x, device)
+    out, code, ldo = _output(o, out, out_dtype, x.dtype, m, n, x, device)
     lib = o.lib
     if workspace is not None:
         ws, have = _workspace(o, workspace, device)
