@@ -325,7 +325,8 @@ rt_status rt_matmul_int8(const int8_t *a, int64_t lda, const float *a_scale, con
  * the quantised activations until its work on `stream` is done: calls that may
  * run at the same time (other streams, other graphs) need one each.
  * rt_linear_int8_workspace returns 0 where none is needed (m = 0, and few or short
- * activations, which one kernel takes whole), -1 for sizes the call refuses.
+ * activations, which one kernel takes whole), -1 for an m, n or k that the call
+ * refuses.  It does not look at m n: above 2^37 the call refuses any workspace.
  */
 int64_t rt_linear_int8_workspace(int64_t m, int64_t n, int32_t k);
 rt_status rt_linear_int8(const void *x, int32_t dtype, int64_t ldx, const int8_t *w, int64_t ldw,

@@ -215,7 +215,8 @@ def linear_int8(x, w, w_scale, bias=None, out=None, out_dtype=None, workspace=No
 
 
 def linear_int8_workspace(m, n, k):
-    """Bytes of workspace linear_int8 needs for m activations of depth k and n rows."""
+    """Bytes of workspace linear_int8 needs for m activations of depth k and n rows
+    (outputs m n above 2^37 have a size here, too, but linear_int8 refuses them)."""
     need = _lib.load().rt_linear_int8_workspace(int(m), int(n), int(k))
     if need < 0:
         raise _lib.ResidentTopKError(_lib.RT_EINVAL, "linear_int8_workspace")
