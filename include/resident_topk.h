@@ -365,7 +365,8 @@ typedef struct {
  * logit above -inf gets token -1 and probability 0.
  * Sums are taken in 64-bit whole multiples of 2^-min(46, 62 - ceil(log2 v)) of
  * the largest weight: the same inputs always give the same token.  A weight is
- * within 2^-43 of itself and half such a unit; below 2^-47 of the largest it is 0.
+ * within 2^-43 of itself and half such a unit (1.1 units where a sum over the
+ * whole row takes it); below 2^-47 of the largest it is 0.
  *   logits    device, r rows of v elements (fp32, bf16 or fp16), ld elements apart
  *   u         device, r fp32 in [0, 1)
  *   out_token device, r int32;  out_prob  device, r fp32, or NULL

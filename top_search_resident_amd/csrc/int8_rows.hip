@@ -102,7 +102,8 @@ __device__ __forceinline__ void codes16(u32x4 v, float s, float inv, uint32_t (&
 
 // One workgroup per row: the largest magnitude, then the codes; the second pass takes up to kQuantKeep chunks per
 // thread from registers and the rest from L2.  Bound by memory for many rows (8192 x 8192 bf16: 35 us, 5.7 TB/s
-// read and written; 2048 x 4096: 7.4 us), by latency for few (1 x 768: 2.6 us).
+// read and written, above a large copy's 5.2 because part of the 134 MB stays in the last-level cache from call to
+// call; 2048 x 4096: 7.4 us), by latency for few (1 x 768: 2.6 us).
 template <typename T>
 __global__ __launch_bounds__(kQuantThreads) void quantize_kernel(const T *x, int64_t ldx, int64_t m, int k,
                                                                  int8_t *q, int64_t ldq, int kpad, float *scale) {
@@ -553,6 +554,8 @@ __global__ __launch_bounds__(1024) void short_kernel(const T *x, int64_t ldx, Pr
 template <typename T, typename O>
 hipError_t launch_few(const void *x, int64_t ldx, const Product &p, hipStream_t s) {
     if (int8_short(p.m, p.n, p.k)) {
+        // up to 33280 bytes of dynamic LDS beside 32896 that the kernel declares: 66176 of a
+        // CU's 163840.  HIP need not be told, as the dynamic part is below 64 KiB.
         const int64_t tiles_n = (p.n + 31) / 32;
         short_kernel<T, O><<<unsigned((p.m + 31) / 32 * tiles_n), 1024, size_t(int8_padded(p.k) + 16) * 32, s>>>(
             static_cast<const T *>(x), ldx, p, int(tiles_n));
@@ -769,18 +772,30 @@ hipError_t launch_product(Product p, hipStream_t s) {
     const bool in_tiles = aligned16(p.a, p.lda) && aligned16(p.b, p.ldb) && p.lda <= (1 << 22) && p.ldb <= (1 << 22) &&
                           tiles(128, 128) < (1 << 22);
     if (p.m <= 16 && (p.n <= 8192 || !in_tiles)) return launch_direct<1, 1, 8, O>(p, s);
+    // Rows that are not aligned have no other way, for any m: no load to LDS takes them.
+    // It is slow, since nothing is reused (us, fp32 out, rows k + 1 bytes apart | aligned):
+    //   16 x 8192 x 4096     31 | 10       500 x 4096 x 4096    170 | 18
+    //   32 x 8192 x 4096     36 | 10       2048 x 4096 x 4096   667 | 45
+    //   77 x 1001 x 777      8.2 | 6.5     500 x 50000 x 768    427 | 47
     if (!in_tiles) return launch_direct<4, 2, 4, O>(p, s);
     // The largest tile, not much higher than m, that still gives each of the 256
-    // CUs one.  Measured (us, fp32 out, bf16 for the first two rows):
-    //   m x n x k             256x256  128x128  128x64  64x64  32x64  32x32  direct
-    //   4 x 8192 x 8192                                 19.0   17.4   16.6   14.0
-    //   32 x 16384 x 4096                               13.7   13.1   13.2   18.8
-    //   8192 x 8192 x 1024    119      121      129     291
-    //   1024 x 8192 x 4096    51.6     39.6     51.7    68.8
-    //   512 x 4096 x 2048              17.3     12.0    12.6   15.0   15.3   21.5
-    //   256 x 4096 x 4096              25.7     16.5    13.7   12.5   15.5   25.9
-    //   1024 x 1024 x 1024             12.4     8.6     7.3    6.6    6.8    10.1
-    //   77 x 1001 x 777                12.6     9.7     9.4    6.6    5.0    6.5
+    // CUs one.  Measured (us, fp32 out; * is what the rule takes):
+    //   m x n x k            256x256 128x128 128x64 64x64  32x128 32x64  32x32  direct
+    //   8192 x 8192 x 1024   119*    121     129    291
+    //   1024 x 8192 x 4096   53      40.9*   51.4   64.4   71     84     99     173
+    //   500 x 50000 x 768    49.4    46.6*   51.8   68.6   71     70     95     138
+    //   512 x 4096 x 2048    33.6    12.5    11.0*  10.1   11.2   13.6   14.7   27.0
+    //   256 x 4096 x 4096    51.3    18.2    15.5   12.7   13.6*  12.0   11.8   25.7
+    //   128 x 8192 x 4096    50.2    25.4    16.3   12.9   13.7*  12.3   13.8   25.9
+    //   64 x 16384 x 4096    48.7    24.6    17.6   14.6   14.2*  13.5   14.8   25.9
+    //   1024 x 1024 x 1024   24.7    9.0     7.5    6.6    6.8*   6.0    6.0    9.3
+    //   64 x 8192 x 4096     48.5    23.5    15.6   12.4   13.4   10.5*  10.8   14.9
+    //   32 x 16384 x 4096    44.0    23.5    16.8   13.7   14.0   12.9*  13.0   21.9
+    //   77 x 1001 x 777      21.3    8.9     7.5    6.9    6.9    5.7    6.6*   7.0
+    //   16 x 100000 x 768    27.0    20.0    21.7   20.0   16.9*  17.2   19.3   28.4
+    //   8 x 32768 x 1024             8.5     8.1    6.1    5.7*   5.7    5.8    13.0
+    // So 32 x 128 is right for a stream of many rows b past few activations, and up to an
+    // eighth slower than 32 x 64 where it takes several tiles of activations.
     if (p.m > 128 && p.k >= 1024 && tiles(256, 256) >= 256) return launch_tile<256, 256, 4, 4, 2, O>(p, s);
     if (p.m > 64 && tiles(128, 128) >= 256) return launch_tile<128, 128, 4, 4, 2, O>(p, s);
     if (p.m > 64 && tiles(128, 64) >= 256) return launch_tile<128, 64, 4, 2, 3, O>(p, s);

@@ -1,5 +1,6 @@
 // large_lds.hpp -- kernels that use more than 64 KiB of dynamic LDS: HIP is told
 // so once per kernel and device (about a microsecond on the calling path each time).
+// What is declared in a kernel does not count there.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>

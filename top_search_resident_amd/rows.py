@@ -8,7 +8,8 @@ next token.  No engine; device tensors in, device tensors out.
 
 Matrices are 2-D with neighbouring elements in a row and any row stride.  The
 work is enqueued on `stream` (default: torch's current stream on the tensors'
-device); tensors made here belong to that stream.
+device); tensors made here belong to that stream.  None of these has a gradient:
+what they return never requires one, whatever the inputs do.
 """
 import ctypes
 
@@ -156,8 +157,8 @@ def quantize_rows_int8(x, out=None, out_scale=None, stream=None):
 def matmul_int8(a, a_scale, b, b_scale, bias=None, out=None, out_dtype=None, stream=None):
     """out[i, j] = sum(a[i] * b[j]) * a_scale[i] * b_scale[j] (+ bias[j]) for int8
     rows a [m, k] and b [n, k] with fp32 scales [m] and [n] and an fp32 bias [n].
-    The sums are exact; the result is rounded once to out_dtype (fp32, bf16 or fp16;
-    default: out's type, or fp32).  Returns out [m, n]."""
+    The sums are exact; what follows them rounds in fp32 step by step, the result once
+    more to out_dtype (fp32, bf16 or fp16; default: out's type, or fp32).  Returns out [m, n]."""
     o = _once if _once.lib else _once.load()
     context = _elsewhere(o, a, "a", stream)
     if context is not None:
